@@ -115,7 +115,8 @@ def source_sha(paths) -> str:
     return h.hexdigest()[:16]
 
 
-GEMM_SOURCES = ["sparse_moe_layer_smoe_b200/csrc/expert_ffn.cu", "sparse_moe_layer_smoe_b200/csrc/common.cuh"]
+GEMM_SOURCES = ["sparse_moe_layer_smoe_b200/csrc/expert_ffn.cu", "sparse_moe_layer_smoe_b200/csrc/expert_gemm.cuh",
+                "sparse_moe_layer_smoe_b200/csrc/common.cuh"]
 
 
 def profiled_traffic(kernel: str, workload: str):

@@ -255,6 +255,93 @@ SMOE_API smoe_status_t smoe_forward_fp8(const smoe_config_t* cfg, const smoe_bf1
                                 const float* w_router, const float* bias, const void* packed_fp8,
                                 smoe_bf16_t* out, void* ws, size_t ws_bytes, void* stream);
 
+/* ---- the backward pass ---------------------------------------------------------------------
+ * Gradients of the layer with respect to x, the router's weights and the experts' weights, given
+ * dout, the gradient of its output [T][H] bf16. A training step chains
+ *   smoe_route (with logits) -> smoe_permute (with x_perm) -> smoe_expert_ffn_save -> smoe_combine
+ *   smoe_combine_backward -> smoe_expert_ffn_backward, smoe_route_backward -> smoe_permute_backward
+ * Sources as for the forward calls (the pages give the layer's formulas; the gradients below follow
+ * from them by differentiation). Gradients of bf16 tensors are bf16, those of fp32 tensors fp32; every
+ * sum is fp32 in a fixed order and rounded once, so results do not depend on scheduling. What a call
+ * writes is overwritten, not added to. Routed rows past offsets[E] (entries that smoe_permute skipped)
+ * are neither read nor written. T == 0 sets the weight gradients to zero. Inputs and outputs must not overlap. The workspace of these calls has
+ * smoe_backward_bytes bytes; one workspace may serve calls that run one after another (a stream, or a
+ * captured graph replayed in stream order), not calls that overlap. Workspace contents are not kept
+ * from one call to the next except the error word. */
+
+/* Bytes of workspace the backward calls need for T tokens. */
+SMOE_API smoe_status_t smoe_backward_bytes(const smoe_config_t* cfg, int64_t T, size_t* bytes);
+
+/* smoe_expert_ffn, which also saves what the backward pass needs of the experts: the gate and up
+ * products g = x W_g^T, u = x W_u^T of every row (before the SwiGLU clamp), in 8 bits.
+ *   gu_q      [T*k + T][2 I] e4m3 codes out (gate features, then up features; rows as those of y)
+ *   gu_scale  [2 I / 32][T*k + T] out: one exponent byte b for each 32 neighbouring features of a row;
+ *             the value held is code * 2^(b - 127), with b the least that brings the 32 magnitudes to
+ *             448 or less (127 if all are 0; at least 1)
+ * Codes are rounded to nearest even from the fp32 accumulators, so a value is held to half a step of
+ * e4m3 (2^-4 relative, 2^-10 of the scale below 2^-6 of it). An infinite or NaN product becomes the
+ * NaN code and does not count in the scale. Other arguments, y and the workspace (smoe_scratch_bytes)
+ * as smoe_expert_ffn; y has the same bits as smoe_expert_ffn's. */
+SMOE_API smoe_status_t smoe_expert_ffn_save(const smoe_config_t* cfg, const smoe_bf16_t* x, const smoe_bf16_t* x_perm,
+                              const int32_t* row_token, const int32_t* offsets, int64_t T, const void* packed,
+                              smoe_bf16_t* y, uint8_t* gu_q, uint8_t* gu_scale, void* ws, size_t ws_bytes,
+                              void* stream);
+
+/* The values a checkpoint stands for: gu [T*k + T][2 I] bf16 out (exact). Needs no workspace. */
+SMOE_API smoe_status_t smoe_checkpoint_values(const smoe_config_t* cfg, const uint8_t* gu_q, const uint8_t* gu_scale,
+                              int64_t T, smoe_bf16_t* gu, void* stream);
+
+/* Gradient of smoe_combine:
+ *   dy[perm_row[t*k + j]] = topk_w[t][j] * dout[t],   dtopk_w[t][j] = <dout[t], y[perm_row[t*k + j]]>
+ *   y        [T*k + T][H] bf16 (the forward pass's), perm_row [T*k] (no row twice), topk_w [T][k] fp32
+ *   dy       [T*k][H] bf16 out, routed rows only: the shared rows' gradient is dout itself
+ *   dtopk_w  [T][k] fp32 out
+ * A perm_row out of range is skipped (its dtopk_w is 0) and sets SMOE_ERR_DEVICE. */
+SMOE_API smoe_status_t smoe_combine_backward(const smoe_config_t* cfg, const smoe_bf16_t* dout, const smoe_bf16_t* y,
+                              const int32_t* perm_row, const float* topk_w, int64_t T, smoe_bf16_t* dy,
+                              float* dtopk_w, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of smoe_route: logits and router weights. With c = route_scale, s = sigmoid(logits):
+ *   dlogits[t][j] = topk_w_j (1 - s_j) sum_i (topk_w_i / c) (dtopk_w_j - dtopk_w_i)
+ *   dw_router[e]  = sum over the entries (t, j) routed to e of dlogits[t][j] * x[t]
+ * (the selection and its bias have no gradient; x's is added by smoe_permute_backward)
+ *   logits [T][E] fp32, topk_idx, topk_w [T][k] (all as smoe_route wrote them), dtopk_w [T][k] fp32,
+ *   offsets [E+1], perm_row, row_token [T*k] (smoe_permute)
+ *   dlogits   [T][k] fp32 out: the gradient of the selected logits (the others' is 0)
+ *   dw_router [E][H] fp32 out (0 for an expert without tokens) */
+SMOE_API smoe_status_t smoe_route_backward(const smoe_config_t* cfg, const smoe_bf16_t* x, int64_t T,
+                              const float* logits, const int32_t* topk_idx, const float* topk_w,
+                              const float* dtopk_w, const int32_t* offsets, const int32_t* perm_row,
+                              const int32_t* row_token, float* dlogits, float* dw_router, void* ws, size_t ws_bytes,
+                              void* stream);
+
+/* Gradient of the experts: from the checkpoint, h = SiLU(g) u, dh = dy W_d, and with s = sigmoid(g)
+ *   dg = dh u s (1 + g (1 - s)),  du = dh g s   (after the SwiGLU clamp; 0 where it cut g or u off)
+ *   dx = dg W_g + du W_u;   dW_g = dg^T x,  dW_u = du^T x,  dW_d = dy^T h over each expert's rows
+ *   x [T][H], x_perm [T*k][H] (smoe_permute), offsets [E+1], packed (smoe_pack_weights),
+ *   gu_q, gu_scale (smoe_expert_ffn_save), dy [T*k][H], dout [T][H] (the shared expert's dy)
+ *   dx_rows  [T*k + T][H] bf16 out: rows as those of y
+ *   dw_gate, dw_up [E][I][H], dw_down [E][H][I], dws_gate, dws_up [Is][H], dws_down [H][Is] bf16 out,
+ *            laid out like smoe_pack_weights' inputs; 0 for an expert without tokens
+ * h, dg and du are rounded to bf16 (they are operands of the tensor-core products that follow). */
+SMOE_API smoe_status_t smoe_expert_ffn_backward(const smoe_config_t* cfg, const smoe_bf16_t* x,
+                              const smoe_bf16_t* x_perm, const int32_t* offsets, int64_t T, const void* packed,
+                              const uint8_t* gu_q, const uint8_t* gu_scale, const smoe_bf16_t* dy,
+                              const smoe_bf16_t* dout, smoe_bf16_t* dx_rows, smoe_bf16_t* dw_gate,
+                              smoe_bf16_t* dw_up, smoe_bf16_t* dw_down, smoe_bf16_t* dws_gate, smoe_bf16_t* dws_up,
+                              smoe_bf16_t* dws_down, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of the layer's input, through the experts (smoe_permute) and the router:
+ *   dx[t] = dx_rows[T*k + t] + sum_j dx_rows[perm_row[t*k + j]] + sum_j dlogits[t][j] * w_router[topk_idx[t][j]]
+ * summed in fp32 and rounded once to bf16. dlogits NULL leaves the router's term out (topk_idx and
+ * w_router are then not read and may be NULL too). An index out of range is skipped and sets
+ * SMOE_ERR_DEVICE.
+ *   dx_rows [T*k + T][H] bf16, w_router [E][H] fp32, dx [T][H] bf16 out */
+SMOE_API smoe_status_t smoe_permute_backward(const smoe_config_t* cfg, const smoe_bf16_t* dx_rows,
+                              const int32_t* perm_row, const int32_t* topk_idx, const float* dlogits,
+                              const float* w_router, int64_t T, smoe_bf16_t* dx, void* ws, size_t ws_bytes,
+                              void* stream);
+
 /* Synchronise `stream` and read the workspace's device error word into *code
  * (SMOE_OK when no kernel recorded an error). */
 SMOE_API smoe_status_t smoe_get_device_error(const void* ws, int32_t* code, void* stream);
@@ -287,7 +374,10 @@ typedef struct {
     char name[32];       /* kernel: router_logits, router_topk, permute_hist, permute_scan,
                             permute_scatter, gather_rows, expert_gateup, expert_down, combine,
                             pack_gateup, pack_down, router_split, router_gemm, diag,
-                            quantize_x, quantize_h, pack_fp8 */
+                            quantize_x, quantize_h, pack_fp8, expert_gateup_save, expert_dh,
+                            expert_dx, expert_wgrad_down, expert_wgrad_gateup, checkpoint_values,
+                            combine_backward, permute_backward, router_dlogits, router_wgrad,
+                            router_wgrad_join */
     int32_t launches;    /* launches recorded */
     float total_ms;      /* summed event-to-event time of those launches */
 } smoe_kernel_time_t;

@@ -37,7 +37,11 @@ const char* const kNames[K_NUM_KERNELS] = {"router_logits", "router_topk",   "pe
                                            "expert_gateup", "expert_down",   "combine",
                                            "pack_gateup",   "pack_down",     "router_split",
                                            "router_gemm",   "diag",        "quantize_x",
-                                           "quantize_h",    "pack_fp8"};
+                                           "quantize_h",    "pack_fp8",    "expert_gateup_save",
+                                           "expert_dh",     "expert_dx",   "expert_wgrad_down",
+                                           "expert_wgrad_gateup", "checkpoint_values", "combine_backward",
+                                           "permute_backward", "router_dlogits", "router_wgrad",
+                                           "router_wgrad_join"};
 }  // namespace
 
 const char* kernel_name(int id) { return (id >= 0 && id < K_NUM_KERNELS) ? kNames[id] : "unknown"; }
@@ -129,6 +133,15 @@ smoe_status_t check_ws(const smoe_config_t* c, int64_t T, const void* ws, size_t
     const WsLayout L = fp8 ? ws_layout_fp8(*c, T, num_sms_current_device()) : ws_layout(*c, T, num_sms_current_device());
     if (ws_bytes < (forward ? L.total : L.scratch_end)) return SMOE_ERR_WORKSPACE;
     return SMOE_OK;
+}
+
+smoe_status_t check_ws_backward(const smoe_config_t* c, int64_t T, const void* ws, size_t ws_bytes) {
+    if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) != 0) return SMOE_ERR_INVALID_ARG;
+    return ws_bytes < bwd_layout(*c, T).total ? SMOE_ERR_WORKSPACE : SMOE_OK;
+}
+
+smoe_status_t zero(void* p, size_t bytes, void* stream) {
+    return cuda_status(cudaMemsetAsync(p, 0, bytes, static_cast<cudaStream_t>(stream)));
 }
 
 template <class T>
@@ -421,6 +434,157 @@ smoe_status_t smoe_forward_diag(const smoe_config_t* c, const smoe_bf16_t* x, in
                                 void* ws, size_t ws_bytes, void* stream) {
     if (diag == nullptr) return SMOE_ERR_INVALID_ARG;
     return forward_impl(c, x, T, w_router, bias, packed, out, diag, ws, ws_bytes, stream);
+}
+
+smoe_status_t smoe_backward_bytes(const smoe_config_t* c, int64_t T, size_t* bytes) {
+    SMOE_TRY(smoe_check_config(c));
+    SMOE_TRY(check_T(c, T));
+    if (bytes == nullptr) return SMOE_ERR_INVALID_ARG;
+    *bytes = bwd_layout(*c, T).total;
+    return SMOE_OK;
+}
+
+smoe_status_t smoe_expert_ffn_save(const smoe_config_t* c, const smoe_bf16_t* x, const smoe_bf16_t* x_perm,
+                                   const int32_t* row_token, const int32_t* offsets, int64_t T, const void* packed,
+                                   smoe_bf16_t* y, uint8_t* gu_q, uint8_t* gu_scale, void* ws, size_t ws_bytes,
+                                   void* stream) {
+    SMOE_TRY(smoe_check_config(c));
+    SMOE_TRY(check_T(c, T));
+    launches_reset();
+    if (T == 0) return SMOE_OK;
+    SMOE_REQUIRE_PTR(x);
+    SMOE_OPTIONAL_PTR(x_perm);
+    SMOE_OPTIONAL_PTR(row_token);
+    if (x_perm == nullptr && row_token == nullptr) return SMOE_ERR_INVALID_ARG;   // one of the two is needed
+    SMOE_REQUIRE_PTR(offsets);
+    SMOE_REQUIRE_PTR(packed);
+    SMOE_REQUIRE_PTR(y);
+    SMOE_REQUIRE_PTR(gu_q);
+    SMOE_REQUIRE_PTR(gu_scale);
+    SMOE_TRY(check_ws(c, T, ws, ws_bytes, false));
+    const int sms = num_sms_current_device();
+    const WsLayout L = ws_layout(*c, T, sms);
+    const Checkpoint ck{gu_q, gu_scale};
+    return cuda_status(launch_expert_ffn(*c, x, x_perm, row_token, offsets, T, packed, y, at<uint16_t>(ws, L.ffn_h),
+                                         at<int32_t>(ws, L.err), sms, static_cast<cudaStream_t>(stream), false, &ck));
+}
+
+smoe_status_t smoe_checkpoint_values(const smoe_config_t* c, const uint8_t* gu_q, const uint8_t* gu_scale, int64_t T,
+                                     smoe_bf16_t* gu, void* stream) {
+    SMOE_TRY(smoe_check_config(c));
+    SMOE_TRY(check_T(c, T));
+    launches_reset();
+    if (T == 0) return SMOE_OK;
+    SMOE_REQUIRE_PTR(gu_q);
+    SMOE_REQUIRE_PTR(gu_scale);
+    SMOE_REQUIRE_PTR(gu);
+    return cuda_status(launch_checkpoint_values(*c, gu_q, gu_scale, T * c->top_k + T, gu,
+                                                static_cast<cudaStream_t>(stream)));
+}
+
+smoe_status_t smoe_combine_backward(const smoe_config_t* c, const smoe_bf16_t* dout, const smoe_bf16_t* y,
+                                    const int32_t* perm_row, const float* topk_w, int64_t T, smoe_bf16_t* dy,
+                                    float* dtopk_w, void* ws, size_t ws_bytes, void* stream) {
+    SMOE_TRY(smoe_check_config(c));
+    SMOE_TRY(check_T(c, T));
+    launches_reset();
+    if (T == 0) return SMOE_OK;
+    SMOE_REQUIRE_PTR(dout);
+    SMOE_REQUIRE_PTR(y);
+    SMOE_REQUIRE_PTR(perm_row);
+    SMOE_REQUIRE_PTR(topk_w);
+    SMOE_REQUIRE_PTR(dy);
+    SMOE_REQUIRE_PTR(dtopk_w);
+    SMOE_TRY(check_ws_backward(c, T, ws, ws_bytes));
+    return cuda_status(launch_combine_backward(*c, dout, y, perm_row, topk_w, T, dy, dtopk_w, at<int32_t>(ws, 0),
+                                               static_cast<cudaStream_t>(stream)));
+}
+
+smoe_status_t smoe_route_backward(const smoe_config_t* c, const smoe_bf16_t* x, int64_t T, const float* logits,
+                                  const int32_t* topk_idx, const float* topk_w, const float* dtopk_w,
+                                  const int32_t* offsets, const int32_t* perm_row, const int32_t* row_token,
+                                  float* dlogits, float* dw_router, void* ws, size_t ws_bytes, void* stream) {
+    SMOE_TRY(smoe_check_config(c));
+    SMOE_TRY(check_T(c, T));
+    launches_reset();
+    if (T == 0) {
+        SMOE_REQUIRE_PTR(dw_router);
+        return zero(dw_router, (size_t)c->n_experts * c->hidden * sizeof(float), stream);
+    }
+    SMOE_REQUIRE_PTR(x);
+    SMOE_REQUIRE_PTR(logits);
+    SMOE_REQUIRE_PTR(topk_idx);
+    SMOE_REQUIRE_PTR(topk_w);
+    SMOE_REQUIRE_PTR(dtopk_w);
+    SMOE_REQUIRE_PTR(offsets);
+    SMOE_REQUIRE_PTR(perm_row);
+    SMOE_REQUIRE_PTR(row_token);
+    SMOE_REQUIRE_PTR(dlogits);
+    SMOE_REQUIRE_PTR(dw_router);
+    SMOE_TRY(check_ws_backward(c, T, ws, ws_bytes));
+    const BwdLayout L = bwd_layout(*c, T);
+    const RouteBackward b{x, logits, topk_idx, topk_w, dtopk_w, offsets, perm_row, row_token, dlogits, dw_router,
+                          at<float>(ws, L.dl_row), at<int4>(ws, L.items), at<int32_t>(ws, L.n_items),
+                          at<float>(ws, L.partial)};
+    return cuda_status(launch_route_backward(*c, b, T, at<int32_t>(ws, L.err), static_cast<cudaStream_t>(stream)));
+}
+
+smoe_status_t smoe_expert_ffn_backward(const smoe_config_t* c, const smoe_bf16_t* x, const smoe_bf16_t* x_perm,
+                                       const int32_t* offsets, int64_t T, const void* packed, const uint8_t* gu_q,
+                                       const uint8_t* gu_scale, const smoe_bf16_t* dy, const smoe_bf16_t* dout,
+                                       smoe_bf16_t* dx_rows, smoe_bf16_t* dw_gate, smoe_bf16_t* dw_up,
+                                       smoe_bf16_t* dw_down, smoe_bf16_t* dws_gate, smoe_bf16_t* dws_up,
+                                       smoe_bf16_t* dws_down, void* ws, size_t ws_bytes, void* stream) {
+    SMOE_TRY(smoe_check_config(c));
+    SMOE_TRY(check_T(c, T));
+    launches_reset();
+    SMOE_REQUIRE_PTR(dw_gate);
+    SMOE_REQUIRE_PTR(dw_up);
+    SMOE_REQUIRE_PTR(dw_down);
+    SMOE_REQUIRE_PTR(dws_gate);
+    SMOE_REQUIRE_PTR(dws_up);
+    SMOE_REQUIRE_PTR(dws_down);
+    if (T == 0) {
+        const size_t one = (size_t)c->inter * c->hidden * sizeof(smoe_bf16_t);
+        for (smoe_bf16_t* w : {dw_gate, dw_up, dw_down}) SMOE_TRY(zero(w, c->n_experts * one, stream));
+        for (smoe_bf16_t* w : {dws_gate, dws_up, dws_down}) SMOE_TRY(zero(w, one, stream));
+        return SMOE_OK;
+    }
+    SMOE_REQUIRE_PTR(x);
+    SMOE_REQUIRE_PTR(x_perm);
+    SMOE_REQUIRE_PTR(offsets);
+    SMOE_REQUIRE_PTR(packed);
+    SMOE_REQUIRE_PTR(gu_q);
+    SMOE_REQUIRE_PTR(gu_scale);
+    SMOE_REQUIRE_PTR(dy);
+    SMOE_REQUIRE_PTR(dout);
+    SMOE_REQUIRE_PTR(dx_rows);
+    SMOE_TRY(check_ws_backward(c, T, ws, ws_bytes));
+    const BwdLayout L = bwd_layout(*c, T);
+    const ExpertBackward b{x, x_perm, offsets, packed, gu_q, gu_scale, dy, dout, dx_rows, dw_gate, dw_up, dw_down,
+                           dws_gate, dws_up, dws_down, at<uint16_t>(ws, L.dgu), at<uint16_t>(ws, L.h)};
+    return cuda_status(launch_expert_ffn_backward(*c, b, T, at<int32_t>(ws, L.err), num_sms_current_device(),
+                                                  static_cast<cudaStream_t>(stream)));
+}
+
+smoe_status_t smoe_permute_backward(const smoe_config_t* c, const smoe_bf16_t* dx_rows, const int32_t* perm_row,
+                                    const int32_t* topk_idx, const float* dlogits, const float* w_router, int64_t T,
+                                    smoe_bf16_t* dx, void* ws, size_t ws_bytes, void* stream) {
+    SMOE_TRY(smoe_check_config(c));
+    SMOE_TRY(check_T(c, T));
+    launches_reset();
+    if (T == 0) return SMOE_OK;
+    SMOE_REQUIRE_PTR(dx_rows);
+    SMOE_REQUIRE_PTR(perm_row);
+    SMOE_OPTIONAL_PTR(dlogits);
+    if (dlogits != nullptr) {
+        SMOE_REQUIRE_PTR(topk_idx);
+        SMOE_REQUIRE_PTR(w_router);
+    }
+    SMOE_REQUIRE_PTR(dx);
+    SMOE_TRY(check_ws_backward(c, T, ws, ws_bytes));
+    return cuda_status(launch_permute_backward(*c, dx_rows, perm_row, topk_idx, dlogits, w_router, T, dx,
+                                               at<int32_t>(ws, 0), static_cast<cudaStream_t>(stream)));
 }
 
 smoe_status_t smoe_selftest_wait_timeout(uint64_t limit_ns, uint64_t* elapsed_ns_opt, void* ws, void* stream) {

@@ -132,6 +132,12 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int32_t
     return mbar_wait_for(bar, parity, err, abort, check_abort, SMOE_WAIT_LIMIT_NS);
 }
 
+// The two e4m3 codes in the low 16 bits (low byte first) as fp32 (exact).
+__device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t codes) {
+    const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3));
+    return __half22float2(h);
+}
+
 // ---------------------------------------------------------------------------------------------
 // TMA (tiled 2D load into shared memory, completion counted on an mbarrier)
 // ---------------------------------------------------------------------------------------------
@@ -310,6 +316,17 @@ __device__ __forceinline__ uint64_t smem_desc_kmajor(uint32_t saddr) {
     d |= layout << 61;
     return d;
 }
+
+// Descriptor of an M- (or N-) major bf16 tile: K rows of 64 M elements (128 bytes, the 128-byte swizzle
+// TMA writes), 8-row atoms of 1024 bytes along K (the stride byte offset), the next 64 M elements
+// m_stride bytes on (the leading byte offset). A K-step of 16 rows adds kMnKStep to the address.
+constexpr uint32_t kMnKStep = 16 * 128;
+constexpr uint32_t kMnBoxBytes = 64 * 128;   // a box of 64 K rows
+__device__ __forceinline__ uint64_t smem_desc_mnmajor(uint32_t saddr, uint32_t m_stride) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(m_stride >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+constexpr uint32_t kIdescAMajorM = 1u << 15, kIdescBMajorN = 1u << 16;   // instruction-descriptor bits
 
 // Instruction descriptor, kind::f16: D fp32 (bits 4-5 = 1), A and B bf16 (bits 7-9, 10-12 = 1),
 // both K-major (bits 15, 16 = 0), N >> 3 at bits 17-22, M >> 4 at bits 24-28.

@@ -82,7 +82,9 @@ void launches_add(int n);
 enum KernelId {
     K_ROUTER_LOGITS = 0, K_ROUTER_TOPK, K_PERMUTE_HIST, K_PERMUTE_SCAN, K_PERMUTE_SCATTER, K_GATHER_ROWS,
     K_EXPERT_GATEUP, K_EXPERT_DOWN, K_COMBINE, K_PACK_GATEUP, K_PACK_DOWN, K_ROUTER_SPLIT, K_ROUTER_GEMM,
-    K_DIAG, K_QUANT_X, K_QUANT_H, K_PACK_FP8, K_NUM_KERNELS
+    K_DIAG, K_QUANT_X, K_QUANT_H, K_PACK_FP8, K_EXPERT_GATEUP_SAVE, K_EXPERT_DH, K_EXPERT_DX, K_EXPERT_WGRAD_DOWN,
+    K_EXPERT_WGRAD_GATEUP, K_CHECKPOINT_VALUES, K_COMBINE_BACKWARD, K_PERMUTE_BACKWARD, K_ROUTER_DLOGITS,
+    K_ROUTER_WGRAD, K_ROUTER_WGRAD_JOIN, K_NUM_KERNELS
 };
 const char* kernel_name(int id);
 
@@ -144,13 +146,67 @@ constexpr int kGatherMaxTile = SMOE_GATHER_MAX_TILE;
 
 // x_perm == nullptr selects gather mode: routed rows are read from x through row_token.
 // Returns cudaErrorNotSupported when the driver entry point for tensor maps is unavailable.
+// ck (smoe_expert_ffn_save): also write the e4m3 checkpoint of the gate and up products.
 // shared_prewait (gather mode): the gate/up kernel computes the shared expert's units before its
 // dependency wait, so x must not come from the two kernels launched just before it; h must
 // not overlap memory those kernels use.
+struct Checkpoint {
+    uint8_t* codes;    // [T*k + T][2 I]
+    uint8_t* scales;   // [2 I / 32][T*k + T]
+};
 cudaError_t launch_expert_ffn(const smoe_config_t& c, const uint16_t* x, const uint16_t* x_perm,
                               const int32_t* row_token, const int32_t* offsets, int64_t T, const void* packed,
                               uint16_t* y, uint16_t* h, int32_t* err, int num_sms, cudaStream_t s,
-                              bool shared_prewait = false);
+                              bool shared_prewait = false, const Checkpoint* ck = nullptr);
+
+// smoe_expert_ffn_backward: inputs, outputs and workspace areas.
+struct ExpertBackward {
+    const uint16_t *x, *x_perm;
+    const int32_t* offsets;
+    const void* packed;
+    const uint8_t *codes, *scales;
+    const uint16_t *dy, *dout;
+    uint16_t *dx_rows, *dw_gate, *dw_up, *dw_down, *dws_gate, *dws_up, *dws_down;
+    uint16_t *dgu, *h;   // workspace: [T*k + T][2 I], [T*k + T][I]
+};
+cudaError_t launch_expert_ffn_backward(const smoe_config_t& c, const ExpertBackward& b, int64_t T, int32_t* err,
+                                       int num_sms, cudaStream_t s);
+
+// Workspace of the backward calls: [error word | the largest of the calls' areas]
+struct BwdLayout {
+    size_t err = 0;
+    size_t dgu = 0, h = 0;                                 // smoe_expert_ffn_backward
+    size_t dl_row = 0, items = 0, n_items = 0, partial = 0;   // smoe_route_backward
+    size_t total = 0;
+};
+BwdLayout bwd_layout(const smoe_config_t& c, int64_t T);
+
+// Router weight gradient: rows of an expert are summed in items of at most this many.
+constexpr int kRouterItemRows = 256;
+inline int64_t router_max_items(int64_t T, int k, int E) { return T * k / kRouterItemRows + E; }
+
+cudaError_t launch_combine_backward(const smoe_config_t& c, const uint16_t* dout, const uint16_t* y,
+                                    const int32_t* perm_row, const float* topk_w, int64_t T, uint16_t* dy,
+                                    float* dtopk_w, int32_t* err, cudaStream_t s);
+cudaError_t launch_permute_backward(const smoe_config_t& c, const uint16_t* dx_rows, const int32_t* perm_row,
+                                    const int32_t* topk_idx, const float* dlogits, const float* w_router, int64_t T,
+                                    uint16_t* dx, int32_t* err, cudaStream_t s);
+struct RouteBackward {
+    const uint16_t* x;
+    const float* logits;
+    const int32_t* topk_idx;
+    const float *topk_w, *dtopk_w;
+    const int32_t *offsets, *perm_row, *row_token;
+    float *dlogits, *dw_router;
+    float* dl_row;       // workspace [T*k]
+    int4* items;         // workspace [router_max_items]: expert, first row, rows, index within the expert
+    int32_t* n_items;    // workspace [E + 1]: first item of each expert, then their number
+    float* partial;      // workspace [router_max_items][H]
+};
+cudaError_t launch_route_backward(const smoe_config_t& c, const RouteBackward& b, int64_t T, int32_t* err,
+                                  cudaStream_t s);
+cudaError_t launch_checkpoint_values(const smoe_config_t& c, const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                     uint16_t* gu, cudaStream_t s);
 
 // row_norm_opt: when set, also ||y[r]||_2 of every routed row r (fp32, [T*k]).
 cudaError_t launch_combine(const smoe_config_t& c, const uint16_t* y, const int32_t* perm_row, const float* topk_w,
