@@ -276,11 +276,12 @@ SMOE_API smoe_status_t smoe_backward_bytes(const smoe_config_t* cfg, int64_t T, 
  * products g = x W_g^T, u = x W_u^T of every row (before the SwiGLU clamp), in 8 bits.
  *   gu_q      [T*k + T][2 I] e4m3 codes out (gate features, then up features; rows as those of y)
  *   gu_scale  [2 I / 32][T*k + T] out: one exponent byte b for each 32 neighbouring features of a row;
- *             the value held is code * 2^(b - 127), with b the least that brings the 32 magnitudes to
- *             448 or less (127 if all are 0; at least 1)
+ *             the value held is code * 2^(b - 127), with b the least, from 1, that brings the 32
+ *             magnitudes to 448 or less
  * Codes are rounded to nearest even from the fp32 accumulators, so a value is held to half a step of
- * e4m3 (2^-4 relative, 2^-10 of the scale below 2^-6 of it). An infinite or NaN product becomes the
- * NaN code and does not count in the scale. Other arguments, y and the workspace (smoe_scratch_bytes)
+ * e4m3 (2^-4 relative, 2^-10 of the scale below 2^-6 of it). An infinite or NaN product is held as
+ * such and gives its block b = 247 or 248, in which its finite neighbours are lost (that row's y is
+ * infinite or NaN all the same). Other arguments, y and the workspace (smoe_scratch_bytes)
  * as smoe_expert_ffn; y has the same bits as smoe_expert_ffn's. */
 SMOE_API smoe_status_t smoe_expert_ffn_save(const smoe_config_t* cfg, const smoe_bf16_t* x, const smoe_bf16_t* x_perm,
                               const int32_t* row_token, const int32_t* offsets, int64_t T, const void* packed,

@@ -23,7 +23,7 @@ def checkpoint(v: np.ndarray):
     b = np.asarray(v, dtype=np.float64).reshape(n, m // BLOCK, BLOCK)
     top = np.abs(b).max(axis=2)
     with np.errstate(divide="ignore"):
-        e = np.ceil(np.log2(np.where(top > 0, top, E4M3_MAX) / E4M3_MAX))
+        e = np.ceil(np.log2(top / E4M3_MAX))
     e = np.maximum(e, -126).astype(np.int64)
     scale = np.exp2(e.astype(np.float64))[:, :, None]
     held = e4m3_round((b / scale).astype(np.float32)) * scale

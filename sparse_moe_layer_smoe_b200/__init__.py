@@ -130,10 +130,22 @@ def _p(t) -> int | None:
     return t.data_ptr()
 
 
+_cuda = None   # torch's current device and, by device, the current stream as an integer (a torch.cuda.Stream
+               # object costs 3 us a call)
+
+
+def _current():
+    global _cuda
+    if _cuda is None:
+        import torch
+        _cuda = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
+    return _cuda
+
+
 def _s(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream or None
+        device, raw_stream = _current()
+        return raw_stream(device()) or None
     if isinstance(stream, int):
         return stream or None
     return stream.cuda_stream or None
@@ -238,32 +250,32 @@ def smoe_forward_fp8(cfg, x, T, w_router, bias, packed_fp8, out, ws=None, ws_byt
                                                       _s(stream)))
 
 
+_dtypes = {}   # name -> torch dtype, filled on the first checked call
+
+
 def _tensors(fn: str, T: int, *args) -> None:
-    """Each (name, tensor, dtype, shape): a torch tensor must hold at least shape's elements of that type,
-    contiguous, on the current CUDA device (whose current stream the call goes to). Raw pointers and None
-    are left to the library's own checks."""
-    import torch
-    here = None
-    for name, t, dtype, shape in args:
-        if t is None or isinstance(t, int):
+    """Each (name, tensor, dtype, n): a torch tensor must hold at least n elements of that type, contiguous,
+    on the current CUDA device (whose current stream the call goes to). Raw pointers and None are left to
+    the library's own checks."""
+    if not _dtypes:
+        import torch
+        _dtypes.update({n: getattr(torch, n) for n in ("bfloat16", "float32", "int32", "uint8")})
+    here = _current()[0]() if T > 0 else None
+    for name, t, dtype, n in args:
+        if t is None or type(t) is int:
             continue
-        n = 1
-        for d in shape:
-            n *= d
-        why = None
-        if t.dtype != getattr(torch, dtype):
+        if (t.dtype is _dtypes[dtype] and t.numel() >= n and t.is_contiguous()
+                and (here is None or t.get_device() == here)):
+            continue
+        if t.dtype is not _dtypes[dtype]:
             why = f"{name} is {t.dtype}, not torch.{dtype}"
         elif not t.is_contiguous():
             why = f"{name} is not contiguous"
         elif t.numel() < n:
-            why = f"{name} has {t.numel()} elements, {list(shape)} needs {n}"
-        elif T > 0:
-            if here is None:
-                here = torch.cuda.current_device()
-            if t.device.type != "cuda" or t.device.index != here:
-                why = f"{name} is on {t.device}, the call runs on cuda:{here}"
-        if why:
-            raise SmoeError(fn, SMOE_ERR_INVALID_ARG, why)
+            why = f"{name} has {t.numel()} elements, {n} are needed"
+        else:
+            why = f"{name} is on {t.device}, the call runs on cuda:{here}"
+        raise SmoeError(fn, SMOE_ERR_INVALID_ARG, why)
 
 
 def smoe_backward_bytes(cfg: SmoeConfig, T: int) -> int:
@@ -274,10 +286,10 @@ def smoe_expert_ffn_save(cfg, x, x_perm, row_token, offsets, T, packed, y, gu_q,
                          stream=None):
     """smoe_expert_ffn with the 8-bit checkpoint of the gate and up products (see include/stepmoe.h)."""
     H, I, R = cfg.hidden, cfg.inter, T * cfg.top_k
-    _tensors("smoe_expert_ffn_save", T, ("x", x, "bfloat16", (T, H)), ("x_perm", x_perm, "bfloat16", (R, H)),
-             ("row_token", row_token, "int32", (R,)), ("offsets", offsets, "int32", (cfg.n_experts + 1,)),
-             ("y", y, "bfloat16", (R + T, H)), ("gu_q", gu_q, "uint8", (R + T, 2 * I)),
-             ("gu_scale", gu_scale, "uint8", (2 * I // 32, R + T)))
+    _tensors("smoe_expert_ffn_save", T, ("x", x, "bfloat16", T * H), ("x_perm", x_perm, "bfloat16", R * H),
+             ("row_token", row_token, "int32", R), ("offsets", offsets, "int32", (cfg.n_experts + 1)),
+             ("y", y, "bfloat16", (R + T) * H), ("gu_q", gu_q, "uint8", (R + T) * 2 * I),
+             ("gu_scale", gu_scale, "uint8", 2 * I // 32 * (R + T)))
     _check("smoe_expert_ffn_save", lib().smoe_expert_ffn_save(ctypes.byref(cfg), _p(x), _p(x_perm), _p(row_token),
                                                               _p(offsets), T, _p(packed), _p(y), _p(gu_q),
                                                               _p(gu_scale), _p(ws), _ws_bytes(ws, ws_bytes),
@@ -287,17 +299,17 @@ def smoe_expert_ffn_save(cfg, x, x_perm, row_token, offsets, T, packed, y, gu_q,
 def smoe_checkpoint_values(cfg, gu_q, gu_scale, T, gu, stream=None):
     """The bf16 values a checkpoint stands for."""
     I, rows = cfg.inter, T * cfg.top_k + T
-    _tensors("smoe_checkpoint_values", T, ("gu_q", gu_q, "uint8", (rows, 2 * I)),
-             ("gu_scale", gu_scale, "uint8", (2 * I // 32, rows)), ("gu", gu, "bfloat16", (rows, 2 * I)))
+    _tensors("smoe_checkpoint_values", T, ("gu_q", gu_q, "uint8", rows * 2 * I),
+             ("gu_scale", gu_scale, "uint8", 2 * I // 32 * rows), ("gu", gu, "bfloat16", rows * 2 * I))
     _check("smoe_checkpoint_values", lib().smoe_checkpoint_values(ctypes.byref(cfg), _p(gu_q), _p(gu_scale), T, _p(gu),
                                                                   _s(stream)))
 
 
 def smoe_combine_backward(cfg, dout, y, perm_row, topk_w, T, dy, dtopk_w, ws=None, ws_bytes=None, stream=None):
     H, k, R = cfg.hidden, cfg.top_k, T * cfg.top_k
-    _tensors("smoe_combine_backward", T, ("dout", dout, "bfloat16", (T, H)), ("y", y, "bfloat16", (R + T, H)),
-             ("perm_row", perm_row, "int32", (R,)), ("topk_w", topk_w, "float32", (T, k)),
-             ("dy", dy, "bfloat16", (R, H)), ("dtopk_w", dtopk_w, "float32", (T, k)))
+    _tensors("smoe_combine_backward", T, ("dout", dout, "bfloat16", T * H), ("y", y, "bfloat16", (R + T) * H),
+             ("perm_row", perm_row, "int32", R), ("topk_w", topk_w, "float32", T * k),
+             ("dy", dy, "bfloat16", R * H), ("dtopk_w", dtopk_w, "float32", T * k))
     _check("smoe_combine_backward", lib().smoe_combine_backward(ctypes.byref(cfg), _p(dout), _p(y), _p(perm_row),
                                                                 _p(topk_w), T, _p(dy), _p(dtopk_w), _p(ws),
                                                                 _ws_bytes(ws, ws_bytes), _s(stream)))
@@ -306,11 +318,11 @@ def smoe_combine_backward(cfg, dout, y, perm_row, topk_w, T, dy, dtopk_w, ws=Non
 def smoe_route_backward(cfg, x, T, logits, topk_idx, topk_w, dtopk_w, offsets, perm_row, row_token, dlogits, dw_router,
                         ws=None, ws_bytes=None, stream=None):
     H, E, k, R = cfg.hidden, cfg.n_experts, cfg.top_k, T * cfg.top_k
-    _tensors("smoe_route_backward", T, ("x", x, "bfloat16", (T, H)), ("logits", logits, "float32", (T, E)),
-             ("topk_idx", topk_idx, "int32", (T, k)), ("topk_w", topk_w, "float32", (T, k)),
-             ("dtopk_w", dtopk_w, "float32", (T, k)), ("offsets", offsets, "int32", (E + 1,)),
-             ("perm_row", perm_row, "int32", (R,)), ("row_token", row_token, "int32", (R,)),
-             ("dlogits", dlogits, "float32", (T, k)), ("dw_router", dw_router, "float32", (E, H)))
+    _tensors("smoe_route_backward", T, ("x", x, "bfloat16", T * H), ("logits", logits, "float32", T * E),
+             ("topk_idx", topk_idx, "int32", T * k), ("topk_w", topk_w, "float32", T * k),
+             ("dtopk_w", dtopk_w, "float32", T * k), ("offsets", offsets, "int32", (E + 1)),
+             ("perm_row", perm_row, "int32", R), ("row_token", row_token, "int32", R),
+             ("dlogits", dlogits, "float32", T * k), ("dw_router", dw_router, "float32", E * H))
     _check("smoe_route_backward", lib().smoe_route_backward(ctypes.byref(cfg), _p(x), T, _p(logits), _p(topk_idx),
                                                             _p(topk_w), _p(dtopk_w), _p(offsets), _p(perm_row),
                                                             _p(row_token), _p(dlogits), _p(dw_router), _p(ws),
@@ -320,13 +332,13 @@ def smoe_route_backward(cfg, x, T, logits, topk_idx, topk_w, dtopk_w, offsets, p
 def smoe_expert_ffn_backward(cfg, x, x_perm, offsets, T, packed, gu_q, gu_scale, dy, dout, dx_rows, dw_gate, dw_up,
                              dw_down, dws_gate, dws_up, dws_down, ws=None, ws_bytes=None, stream=None):
     H, E, I, R = cfg.hidden, cfg.n_experts, cfg.inter, T * cfg.top_k
-    _tensors("smoe_expert_ffn_backward", T, ("x", x, "bfloat16", (T, H)), ("x_perm", x_perm, "bfloat16", (R, H)),
-             ("offsets", offsets, "int32", (E + 1,)), ("gu_q", gu_q, "uint8", (R + T, 2 * I)),
-             ("gu_scale", gu_scale, "uint8", (2 * I // 32, R + T)), ("dy", dy, "bfloat16", (R, H)),
-             ("dout", dout, "bfloat16", (T, H)), ("dx_rows", dx_rows, "bfloat16", (R + T, H)),
-             ("dw_gate", dw_gate, "bfloat16", (E, I, H)), ("dw_up", dw_up, "bfloat16", (E, I, H)),
-             ("dw_down", dw_down, "bfloat16", (E, H, I)), ("dws_gate", dws_gate, "bfloat16", (I, H)),
-             ("dws_up", dws_up, "bfloat16", (I, H)), ("dws_down", dws_down, "bfloat16", (H, I)))
+    _tensors("smoe_expert_ffn_backward", T, ("x", x, "bfloat16", T * H), ("x_perm", x_perm, "bfloat16", R * H),
+             ("offsets", offsets, "int32", (E + 1)), ("gu_q", gu_q, "uint8", (R + T) * 2 * I),
+             ("gu_scale", gu_scale, "uint8", 2 * I // 32 * (R + T)), ("dy", dy, "bfloat16", R * H),
+             ("dout", dout, "bfloat16", T * H), ("dx_rows", dx_rows, "bfloat16", (R + T) * H),
+             ("dw_gate", dw_gate, "bfloat16", E * I * H), ("dw_up", dw_up, "bfloat16", E * I * H),
+             ("dw_down", dw_down, "bfloat16", E * H * I), ("dws_gate", dws_gate, "bfloat16", I * H),
+             ("dws_up", dws_up, "bfloat16", I * H), ("dws_down", dws_down, "bfloat16", H * I))
     _check("smoe_expert_ffn_backward", lib().smoe_expert_ffn_backward(
         ctypes.byref(cfg), _p(x), _p(x_perm), _p(offsets), T, _p(packed), _p(gu_q), _p(gu_scale), _p(dy), _p(dout),
         _p(dx_rows), _p(dw_gate), _p(dw_up), _p(dw_down), _p(dws_gate), _p(dws_up), _p(dws_down), _p(ws),
@@ -336,10 +348,10 @@ def smoe_expert_ffn_backward(cfg, x, x_perm, offsets, T, packed, gu_q, gu_scale,
 def smoe_permute_backward(cfg, dx_rows, perm_row, topk_idx, dlogits, w_router, T, dx, ws=None, ws_bytes=None,
                           stream=None):
     H, E, k, R = cfg.hidden, cfg.n_experts, cfg.top_k, T * cfg.top_k
-    _tensors("smoe_permute_backward", T, ("dx_rows", dx_rows, "bfloat16", (R + T, H)),
-             ("perm_row", perm_row, "int32", (R,)), ("topk_idx", topk_idx, "int32", (T, k)),
-             ("dlogits", dlogits, "float32", (T, k)), ("w_router", w_router, "float32", (E, H)),
-             ("dx", dx, "bfloat16", (T, H)))
+    _tensors("smoe_permute_backward", T, ("dx_rows", dx_rows, "bfloat16", (R + T) * H),
+             ("perm_row", perm_row, "int32", R), ("topk_idx", topk_idx, "int32", T * k),
+             ("dlogits", dlogits, "float32", T * k), ("w_router", w_router, "float32", E * H),
+             ("dx", dx, "bfloat16", T * H))
     _check("smoe_permute_backward", lib().smoe_permute_backward(ctypes.byref(cfg), _p(dx_rows), _p(perm_row),
                                                                 _p(topk_idx), _p(dlogits), _p(w_router), T, _p(dx),
                                                                 _p(ws), _ws_bytes(ws, ws_bytes), _s(stream)))

@@ -410,6 +410,21 @@ __device__ __forceinline__ void umma_commit_pair(uint32_t cluster_addr) {
                  : "memory");
 }
 
+// The same, arriving on the barrier at this shared-memory offset in both CTAs of the pair.
+__device__ __forceinline__ void umma_commit_pair_both(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+// True in one lane of a converged warp (the same one on every call).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // Tiled 2D load into this CTA's shared memory whose completed bytes are counted on an mbarrier of
 // the first CTA of the pair (cluster-window address `bar_leader`).
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int32_t c0, int32_t c1,

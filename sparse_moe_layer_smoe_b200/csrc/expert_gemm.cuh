@@ -386,71 +386,63 @@ __device__ __forceinline__ void epi_store(const uint32_t (&hv)[16 * NS], int nch
     }
 }
 
-// Checkpoint scale of 32 neighbouring features of one row, from the bits of the largest finite
-// magnitude among them: the exponent byte of the least power of two that brings it to 448 or less
-// (448 = 1.75 * 2^8), 127 (factor 1) for all zeros. A power of two costs e4m3 no precision (codes are
-// floating) and makes scaling and rescaling exact.
+// Checkpoint scale of 32 neighbouring features of one row, from the bits of the largest magnitude among
+// them: the exponent byte of the least power of two, from 2^-126, that brings it to 448 or less
+// (448 = 1.75 * 2^8: the addition carries into the exponent where the mantissa is above 0.75). A power of
+// two costs e4m3 no precision (codes are floating) and makes scaling and rescaling exact.
 __device__ __forceinline__ uint32_t ck_scale_byte(uint32_t absmax_bits) {
-    const int e = (int)(absmax_bits >> 23) - 8 + ((absmax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-    return absmax_bits == 0 ? 127u : (uint32_t)max(e, 1);
+    return max((absmax_bits + 0x1FFFFFu) >> 23, 9u) - 8u;
 }
 
-// Saving gate/up, part 1: drains the accumulators like epi_load and also writes the checkpoint of the
+// Columns of a unit that a training epilogue takes at a time. Its loop over them is not unrolled: with
+// every column of a unit unrolled (as epi_load is, for far fewer instructions a column) the code
+// outgrows the instruction cache, and the warps spend most of their time waiting for instructions.
+constexpr int kTrainCols = 16;
+
+// Saving gate/up: drains the accumulators like epi_load and epi_store, and writes the checkpoint of the
 // products before the clamp: a warp holds 32 neighbouring features (lanes) of a token column, so the
-// largest magnitude is one warp reduction over the magnitudes' bits (ordered like the values).
-// Infinities and NaN become the NaN code (and do not count in the scale). f = this thread's feature.
-template <int NS = 8>
-__device__ __forceinline__ void epi_load_save(const GemmParams& p, uint32_t t_row, int nch, int nvalid, float lim,
-                                              uint32_t (&hv)[16 * NS], int64_t row0, int f, int lane, int c0 = 0) {
+// largest magnitude is one warp reduction over the magnitudes' bits (ordered like the values). An
+// infinite or NaN product has bits above every finite one's and gives its block the scale 2^120, in
+// which an infinity is held as infinite (448 * 2^120 overflows fp32). f = this thread's feature; the
+// G warps of a TMEM lane quarter take every G-th group of columns, c0 = this warp's first.
+template <int G>
+__device__ __forceinline__ void epi_gateup_save(const GemmParams& p, uint32_t t_row, int nvalid, float lim, int64_t row0,
+                                                int f, int lane, int c0) {
     const int I = p.n_out;
     uint8_t* code_g = p.codes + (size_t)row0 * (2 * I) + f;
     uint8_t* scale_g = p.scales + (size_t)(f / 32) * p.ck_rows + row0;
     uint8_t* scale_u = scale_g + (size_t)(I / 32) * p.ck_rows;
+    uint16_t* h_out = p.out + (size_t)row0 * I + f;
+#pragma unroll 1
+    for (int c = c0 * kTrainCols; c < nvalid; c += G * kTrainCols) {
+        uint32_t a[kTrainCols], b[kTrainCols];
+        tmem_ld2_x16_wait(t_row + c, t_row + p.nt_max + c, a, b);
+        uint32_t sb_g = 0, sb_u = 0;   // lane j: the scale bytes of column c + j
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-        const int c = c0 + (8 / NS) * i;
-        if (c < nch) {
-            uint32_t a[32], b[32];
-            tmem_ld2_x32_wait(t_row + 32 * c, t_row + p.nt_max + 32 * c, a, b);
-            uint32_t sb_g = 0, sb_u = 0;   // lane j: the scale bytes of column 32 c + j
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const uint32_t mg = a[j] & 0x7FFFFFFFu, mu = b[j] & 0x7FFFFFFFu;
-                const uint32_t eg = ck_scale_byte(__reduce_max_sync(0xFFFFFFFFu, mg < 0x7F800000u ? mg : 0u));
-                const uint32_t eu = ck_scale_byte(__reduce_max_sync(0xFFFFFFFFu, mu < 0x7F800000u ? mu : 0u));
-                if (lane == j) {
-                    sb_g = eg;
-                    sb_u = eu;
-                }
-                const float g = __uint_as_float(a[j]), u = __uint_as_float(b[j]);
-                // v * 0 adds nothing to a finite product and turns an infinite one into NaN
-                const float2 q = make_float2(fmaf(g, 0.f, g * __uint_as_float((254u - eg) << 23)),
-                                             fmaf(u, 0.f, u * __uint_as_float((254u - eu) << 23)));
-                const uint32_t two = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
-                if (32 * c + j < nvalid) {
-                    uint8_t* d = code_g + (size_t)(32 * c + j) * (2 * I);
-                    d[0] = (uint8_t)two;
-                    d[I] = (uint8_t)(two >> 8);
-                }
+        for (int j = 0; j < kTrainCols; ++j) {
+            const uint32_t eg = ck_scale_byte(__reduce_max_sync(0xFFFFFFFFu, a[j] & 0x7FFFFFFFu));
+            const uint32_t eu = ck_scale_byte(__reduce_max_sync(0xFFFFFFFFu, b[j] & 0x7FFFFFFFu));
+            if (lane == j) {
+                sb_g = eg;
+                sb_u = eu;
             }
-            if (32 * c + lane < nvalid) {
-                scale_g[32 * c + lane] = (uint8_t)sb_g;
-                scale_u[32 * c + lane] = (uint8_t)sb_u;
+            float g = __uint_as_float(a[j]), u = __uint_as_float(b[j]);
+            const float2 q = make_float2(g * __uint_as_float((254u - eg) << 23), u * __uint_as_float((254u - eu) << 23));
+            const uint32_t two = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+            if (lim > 0.0f) {
+                g = fminf(g, lim);
+                u = fminf(fmaxf(u, -lim), lim);
             }
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                float v[2];
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    float g = __uint_as_float(a[2 * j + z]), u = __uint_as_float(b[2 * j + z]);
-                    if (lim > 0.0f) {
-                        g = fminf(g, lim);
-                        u = fminf(fmaxf(u, -lim), lim);
-                    }
-                    v[z] = silu_mul(g, u);
-                }
-                hv[16 * i + j] = pack_bf16x2(v[0], v[1]);
+            if (c + j < nvalid) {
+                uint8_t* d = code_g + (size_t)(c + j) * (2 * I);
+                d[0] = (uint8_t)two;
+                d[I] = (uint8_t)(two >> 8);
+                h_out[(size_t)(c + j) * I] = float_to_bf16_bits(silu_mul(g, u));
             }
+        }
+        if (lane < kTrainCols && c + lane < nvalid) {
+            scale_g[c + lane] = (uint8_t)sb_g;
+            scale_u[c + lane] = (uint8_t)sb_u;
         }
     }
 }
@@ -459,58 +451,55 @@ __device__ __forceinline__ void epi_load_save(const GemmParams& p, uint32_t t_ro
 // to [-L, L] under a clamp), s = sigmoid(g') and the accumulator dh:
 //   h = g' s u',  dg = dh u' s (1 + g' (1 - s)) where g <= L,  du = dh g' s where |u| <= L, else 0
 // computed in fp32 and rounded once to bf16 (h, dg and du are operands of bf16 products next).
-template <int NS = 8>
-__device__ __forceinline__ void epi_swiglu_backward(const GemmParams& p, uint32_t t_row, int nch, int nvalid, float lim,
-                                                    int64_t row0, int f, int lane, int c0 = 0) {
+template <int G>
+__device__ __forceinline__ void epi_swiglu_backward(const GemmParams& p, uint32_t t_row, int nvalid, float lim,
+                                                    int64_t row0, int f, int lane, int c0) {
     const int I = p.n_out;
     const uint8_t* code_g = p.codes + (size_t)row0 * (2 * I) + f;
     const uint8_t* scale_g = p.scales + (size_t)(f / 32) * p.ck_rows + row0;
     const uint8_t* scale_u = scale_g + (size_t)(I / 32) * p.ck_rows;
     uint16_t* dg_out = p.out + (size_t)row0 * (2 * I) + f;
     uint16_t* h_out = p.h_out + (size_t)row0 * I + f;
+#pragma unroll 1
+    for (int c = c0 * kTrainCols; c < nvalid; c += G * kTrainCols) {
+        uint32_t code[kTrainCols];   // gate code in the low byte, up code above it
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-        const int c = c0 + (8 / NS) * i;
-        if (c < nch) {
-            uint32_t code[32];   // gate code in the low byte, up code above it
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                code[j] = 0;
-                if (32 * c + j < nvalid) {
-                    const uint8_t* s = code_g + (size_t)(32 * c + j) * (2 * I);
-                    code[j] = (uint32_t)s[0] | ((uint32_t)s[I] << 8);
-                }
+        for (int j = 0; j < kTrainCols; ++j) {
+            code[j] = 0;
+            if (c + j < nvalid) {
+                const uint8_t* s = code_g + (size_t)(c + j) * (2 * I);
+                code[j] = (uint32_t)s[0] | ((uint32_t)s[I] << 8);
             }
-            float sg = 0.f, su = 0.f;   // lane j: the scales of column 32 c + j
-            if (32 * c + lane < nvalid) {
-                sg = __uint_as_float((uint32_t)scale_g[32 * c + lane] << 23);
-                su = __uint_as_float((uint32_t)scale_u[32 * c + lane] << 23);
-            }
-            uint32_t a[32];
-            tmem_ld_x32_wait(t_row + 32 * c, a);
+        }
+        float sg = 0.f, su = 0.f;   // lane j: the scales of column c + j
+        if (lane < kTrainCols && c + lane < nvalid) {
+            sg = __uint_as_float((uint32_t)scale_g[c + lane] << 23);
+            su = __uint_as_float((uint32_t)scale_u[c + lane] << 23);
+        }
+        uint32_t a[kTrainCols];
+        tmem_ld_x16_wait(t_row + c, a);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const float kg = __shfl_sync(0xFFFFFFFFu, sg, j), ku = __shfl_sync(0xFFFFFFFFu, su, j);
-                if (32 * c + j < nvalid) {
-                    const float2 q = e4m3x2_to_float2(code[j]);
-                    float g = q.x * kg, u = q.y * ku;
-                    bool pass_g = true, pass_u = true;
-                    if (lim > 0.0f) {
-                        pass_g = !(g > lim);
-                        pass_u = !(fabsf(u) > lim);
-                        g = fminf(g, lim);
-                        u = fminf(fmaxf(u, -lim), lim);
-                    }
-                    const float dh = __uint_as_float(a[j]);
-                    const float s = __fdividef(1.0f, 1.0f + __expf(-g));
-                    const float gs = g * s;
-                    const float dg = pass_g ? dh * u * (s + gs * (1.0f - s)) : 0.0f;
-                    const float du = pass_u ? dh * gs : 0.0f;
-                    uint16_t* d = dg_out + (size_t)(32 * c + j) * (2 * I);
-                    d[0] = float_to_bf16_bits(dg);
-                    d[I] = float_to_bf16_bits(du);
-                    h_out[(size_t)(32 * c + j) * I] = float_to_bf16_bits(gs * u);
+        for (int j = 0; j < kTrainCols; ++j) {
+            const float kg = __shfl_sync(0xFFFFFFFFu, sg, j), ku = __shfl_sync(0xFFFFFFFFu, su, j);
+            if (c + j < nvalid) {
+                const float2 q = e4m3x2_to_float2(code[j]);
+                float g = q.x * kg, u = q.y * ku;
+                bool pass_g = true, pass_u = true;
+                if (lim > 0.0f) {
+                    pass_g = !(g > lim);
+                    pass_u = !(fabsf(u) > lim);
+                    g = fminf(g, lim);
+                    u = fminf(fmaxf(u, -lim), lim);
                 }
+                const float dh = __uint_as_float(a[j]);
+                const float s = __fdividef(1.0f, 1.0f + __expf(-g));
+                const float gs = g * s;
+                const float dg = pass_g ? dh * u * (s + gs * (1.0f - s)) : 0.0f;
+                const float du = pass_u ? dh * gs : 0.0f;
+                uint16_t* d = dg_out + (size_t)(c + j) * (2 * I);
+                d[0] = float_to_bf16_bits(dg);
+                d[I] = float_to_bf16_bits(du);
+                h_out[(size_t)(c + j) * I] = float_to_bf16_bits(gs * u);
             }
         }
     }
@@ -828,9 +817,12 @@ expert_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmParams p) {
                 }
                 tc_fence_before();
                 mbar_arrive(smem_u32(&tempty[acc]));
-            } else if (MODE == MODE_DH) {
-                epi_swiglu_backward(p, t_row, (nvalid + 31) / 32, nvalid, w.g < E ? p.clamp_routed : p.clamp_shared,
-                                    out_base, f, lane);
+            } else if constexpr (MODE == MODE_DH || MODE == MODE_GATEUP_SAVE) {
+                const float lim = w.g < E ? p.clamp_routed : p.clamp_shared;
+                if constexpr (MODE == MODE_DH)
+                    epi_swiglu_backward<1>(p, t_row, nvalid, lim, out_base, f, lane, 0);
+                else
+                    epi_gateup_save<1>(p, t_row, nvalid, lim, out_base, f, lane, 0);
                 tc_fence_before();
                 mbar_arrive(smem_u32(&tempty[acc]));
             } else {
@@ -841,11 +833,8 @@ expert_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmParams p) {
                     rs_g = p.w_scale[(size_t)(DUAL ? 2 * w.g : w.g) * p.n_out + f];
                     if (DUAL) rs_u = p.w_scale[(size_t)(2 * w.g + 1) * p.n_out + f];
                 }
-                const float lim = w.g < E ? p.clamp_routed : p.clamp_shared;
-                if constexpr (MODE == MODE_GATEUP_SAVE)
-                    epi_load_save(p, t_row, nch, nvalid, lim, hv, out_base, f, lane);
-                else
-                    epi_load<DUAL, F8>(t_row, p.nt_max, nch, lim, hv, rs_g, rs_u, cs);
+                epi_load<DUAL, F8>(t_row, p.nt_max, nch, w.g < E ? p.clamp_routed : p.clamp_shared, hv, rs_g, rs_u,
+                                   cs);
                 tc_fence_before();
                 mbar_arrive(smem_u32(&tempty[acc]));   // accumulator free before the stores
                 epi_store(hv, nch, nvalid, p.out, dst0, p.out_ld);
@@ -1140,9 +1129,9 @@ expert_gemm_pair_kernel(const __grid_constant__ GemmMaps maps, const GemmParams 
                 if (DUAL) rs_u = p.w_scale[(size_t)(2 * w.g + 1) * p.n_out + f];
             }
             if constexpr (MODE == MODE_DH)
-                epi_swiglu_backward<NS>(p, t_row, nch, nvalid, lim, out_base, f, lane, c0);
+                epi_swiglu_backward<G>(p, t_row, nvalid, lim, out_base, f, lane, c0);
             else if constexpr (MODE == MODE_GATEUP_SAVE)
-                epi_load_save<NS>(p, t_row, nch, nvalid, lim, hv, out_base, f, lane, c0);
+                epi_gateup_save<G>(p, t_row, nvalid, lim, out_base, f, lane, c0);
             else
                 epi_load<DUAL, F8, NS>(t_row, p.nt_max, nch, lim, hv, rs_g, rs_u, cs, c0);
             tc_fence_before();
@@ -1150,7 +1139,7 @@ expert_gemm_pair_kernel(const __grid_constant__ GemmMaps maps, const GemmParams 
             // accumulator free: every lane's TMEM loads have completed (tcgen05.wait::ld), so the
             // arrive needs no release; a release would first wait for the previous unit's stores
             if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&tempty[acc]), 0));
-            if constexpr (MODE != MODE_DH) epi_store<NS>(hv, nch, nvalid, p.out, dst0, p.out_ld, c0);
+            if constexpr (MODE != MODE_DH && MODE != MODE_GATEUP_SAVE) epi_store<NS>(hv, nch, nvalid, p.out, dst0, p.out_ld, c0);
             if (NACC == 2) {
                 acc ^= 1;
                 if (acc == 0) acc_phase ^= 1u;

@@ -6,31 +6,36 @@
 // (SwiGLU experts: Step 3.5 Flash summary, paperlayer.ai, §B.) dh and dx run on the forward pass's
 // kernels and read its packed weights in place, through M-major operand tiles.
 //
-// Weight gradients: a persistent, warp-specialised grouped GEMM whose contraction runs over an
-// expert's rows. Unit = (group, 128 x 256 block of the gradient); both operands are M-major tiles of
-// 64 rows x 64 columns boxes straight from the row-major activations, so nothing is transposed. A
-// group's rows start anywhere and rarely end on a tile: the last stage also holds rows of the next
-// group, which may be infinite or NaN, so up to the next multiple of 16 they are overwritten with
-// zeros in shared memory and the products beyond are not issued. Groups without rows get zeros.
+// Weight gradients: a persistent, warp-specialised grouped GEMM on CTA pairs whose contraction runs over
+// an expert's rows. Unit = (group, 256 x 256 block of the gradient); both operands are M-major tiles
+// (boxes of 64 rows x 64 columns) straight from the row-major activations, so nothing is transposed.
+// Every CTA of the pair loads 128 of the block's rows' columns and 128 of its columns': 32 KB a stage for
+// 512 clocks of MMA, where one CTA alone on 128 x 256 would load 48 KB and is bound by L2 (measured 3.9 ms
+// against the pair's time below). A group's rows start anywhere and rarely end on a tile: the last stage
+// also holds rows of the next group, which may be infinite or NaN, so up to the next multiple of 16 they
+// are overwritten with zeros in shared memory and the products beyond are not issued. Groups without
+// rows get zeros.
 #include "expert_gemm.cuh"
 
 namespace smoe {
 
 namespace {
 
-constexpr int kWgThreads = 192;      // producer warp, MMA warp, four epilogue warps
-constexpr int kWgN = 256;            // gradient columns of a unit (128 for the last block of an odd width)
+constexpr int kWgEpiWarps = 8;       // two per quarter of the TMEM lanes, each every other 64-column box
+constexpr int kWgThreads = 128 + 32 * kWgEpiWarps;  // two producer warps, MMA and tail warp, epilogue warps
+constexpr int kWgTile = 256;         // gradient rows (128 a CTA) and columns of a unit
 constexpr int kWgKRows = 64;         // rows of a pipeline stage
-constexpr int kWgABytes = 2 * kMnBoxBytes;
-constexpr int kWgStageBytes = kWgABytes + (kWgN / 64) * kMnBoxBytes;
-constexpr int kWgStages = 4;
-constexpr int kWgStoreBytes = 32 * 128;   // an epilogue warp's staging box: 32 gradient rows x 64 columns
+constexpr int kWgABytes = 2 * kMnBoxBytes;          // this CTA's 128 gradient rows
+constexpr int kWgStageBytes = 2 * kWgABytes;        // and its half of the columns
+constexpr int kWgMaxStages = 6;
+constexpr int kWgStoreBytes = 32 * 128;   // an epilogue warp's staging box (two each): 32 gradient rows x 64 columns
 
 struct WgradMaps {
-    CUtensorMap a, a_sh;        // M side [rows][M] of the routed groups and of the shared one: box {64, 64}
-    CUtensorMap b, b_sh;        // N side [rows][N]: box {64, 64}
+    // operands [rows][cols] viewed as {64 columns, rows, cols / 64}, box {64, 64, 2}: two M-major tiles a load
+    CUtensorMap a, a_sh;        // M side of the routed groups and of the shared one
+    CUtensorMap b, b_sh;        // N side
     CUtensorMap out[2];         // gradients [E * M'][N]: rows m < m_split go to out[0], the others to out[1]
-    CUtensorMap out_sh[2];      // the shared expert's [M'][N]: box {64, 32}
+    CUtensorMap out_sh[2];      // the shared expert's [M'][N]; boxes of 64 columns x 32 rows
 };
 
 struct WgradParams {
@@ -39,6 +44,8 @@ struct WgradParams {
     int M, N;                 // gradient rows (over both outputs) and columns
     int m_split;              // rows of an output (M or M / 2)
     int a_sh_row, b_sh_row;   // first row of the shared group in a_sh / b_sh
+    int stages;               // pipeline depth
+    uint32_t inv_nb, inv_upg; // 2^32 / (column blocks), 2^32 / (units of a group), rounded up
     int32_t* err;
 };
 
@@ -49,19 +56,55 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int32_t c0,
                  : "memory");
 }
 
-size_t wgrad_smem_bytes(int E) {
-    return 1024 + (size_t)kWgStages * kWgStageBytes + 4 * kWgStoreBytes + sizeof(uint64_t) * (2 * kWgStages + 5) + 16 +
-           sizeof(int32_t) * (size_t)(E + 1);
+// Operand map (see WgradMaps) of a bf16 matrix [rows][cols], cols a multiple of 64.
+bool make_wgrad_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {64, rows, cols / 64};
+    cuuint64_t strides[2] = {cols * 2, 128};
+    cuuint32_t box[3] = {64, kWgKRows, 2};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-__global__ void __launch_bounds__(kWgThreads, 1)
+// tma_load_2d_pair for a 3D map.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, int32_t c0, int32_t c1, int32_t c2,
+                                                 uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
+        : "memory");
+}
+
+size_t wgrad_smem_bytes(int stages, int E) {
+    return 1024 + (size_t)stages * kWgStageBytes + 2 * kWgEpiWarps * kWgStoreBytes +
+           sizeof(uint64_t) * (4 * (size_t)stages + 5) + 16 + sizeof(int32_t) * (size_t)(E + 1);
+}
+
+// Arrive on an mbarrier of the pair's first CTA. What it orders are writes to this CTA's own shared memory,
+// which fence.proxy.async has already made visible to the tensor cores; a release at cluster scope on top
+// measured 1150 clocks.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1)
 expert_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradParams p) {
     extern __shared__ uint8_t smem_raw[];
-    constexpr int S = kWgStages;
+    const int S = p.stages;
     uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* staging = tiles + (size_t)S * kWgStageBytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(staging + 4 * kWgStoreBytes);
-    uint64_t* empty = full + S;
+    uint64_t* full = reinterpret_cast<uint64_t*>(staging + 2 * kWgEpiWarps * kWgStoreBytes);
+    // A stage's loads of both CTAs complete on the first CTA's full barrier. A stage with a row tail is
+    // different: each CTA's loads complete on its own tail_full and its tail warp clears the tail; the
+    // second CTA's then arrives on the first one's tail_ready, and the first one's, having seen that, on
+    // full. The MMA thread waits for full alone, and the clearing is done well before it gets there.
+    uint64_t* tail_full = full + S;
+    uint64_t* tail_ready = tail_full + S;
+    uint64_t* empty = tail_ready + S;
     uint64_t* tfull = empty + S;
     uint64_t* tempty = tfull + 2;
     uint64_t* drain = tempty + 2;
@@ -70,28 +113,31 @@ expert_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradParams p)
     int32_t* offs = reinterpret_cast<int32_t*>(tmem_slot + 4);   // [E+1]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_ctarank();
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
     const int E = p.E;
-    const int MB = p.M / 128, NB = (p.N + kWgN - 1) / kWgN;
+    const int MB = (p.M + kWgTile - 1) / kWgTile, NB = (p.N + kWgTile - 1) / kWgTile;
     const int upg = MB * NB;                 // units of a group
-    const int total = (E + 1) * upg;         // at most 1025 * 512 * 128: fits
-    const int W = gridDim.x;
+    const int total = (E + 1) * upg;         // at most 1025 * 256 * 128: fits
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&tail_full[s]), 1);
+            mbar_init(smem_u32(&tail_ready[s]), 1);
             mbar_init(smem_u32(&empty[s]), 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(smem_u32(&tfull[a]), 1);
-            mbar_init(smem_u32(&tempty[a]), 4);
+            mbar_init(smem_u32(&tempty[a]), 2 * kWgEpiWarps);   // epilogue warps of both CTAs
         }
         mbar_init(smem_u32(drain), 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
     if (warp == 0) {
-        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
-        tmem_relinquish();
+        tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish_pair();
     }
     pdl_wait();
     pdl_launch_dependents();
@@ -112,130 +158,207 @@ expert_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradParams p)
         }
     }
     tc_fence_before();
-    __syncthreads();
+    cluster_sync();   // barrier inits and TMEM allocation visible to both CTAs
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
     // unit u: the shared group's first (it has the most rows), then the routed groups in order; the
-    // units of a group run at the same time on neighbouring SMs and share its rows in L2
+    // units of a group run at the same time on neighbouring pairs and share its rows in L2
     struct WUnit { int g, mb, nb, rows, ncols; };
+    // a / b by its rounded-up reciprocal: one too high at most (a < 2^32), which the remainder shows
+    auto divide = [](int a, int b, uint32_t inv, int& rest) {
+        int q = b == 1 ? a : (int)__umulhi((uint32_t)a, inv);
+        rest = a - q * b;
+        if (rest < 0) {
+            --q;
+            rest += b;
+        }
+        return q;
+    };
     auto unit_at = [&](int u) {
         WUnit w;
-        const int o = u / upg, r = u % upg;
+        int r;
+        const int o = divide(u, upg, p.inv_upg, r);
         w.g = o == 0 ? E : o - 1;
-        w.mb = r / NB;
-        w.nb = r % NB;
+        w.mb = divide(r, NB, p.inv_nb, w.nb);
         w.rows = group_rows(w.g, E, p.T, offs);
-        w.ncols = min(kWgN, p.N - w.nb * kWgN);
+        w.ncols = min(kWgTile, p.N - w.nb * kWgTile);
         return w;
     };
+    auto is_tail = [](int rows, int k) { return k + kWgKRows > rows && ((rows - k) & 15) != 0; };
 
-    if (warp == 0 && lane == 0) {
-        // ---------------------------------------------------------------- TMA producer
+    if ((warp == 0 || warp == 3) && lane == 0) {
+        // ---------------------------------------------------------------- TMA producers (both CTAs)
+        // warp 0 arms a stage's barrier and loads the M side, warp 3 the N side (one thread doing both
+        // could not issue fast enough: 1350 clocks a stage, 180 of them for each 8 KB box). Bytes may
+        // land before the barrier is armed; the phase waits for the arming arrival.
+        const bool m_side = warp == 0;
         const uint64_t pol = l2_policy_evict_last();
+        const CUtensorMap* const routed_map = m_side ? &maps.a : &maps.b;
+        const CUtensorMap* const shared_map = m_side ? &maps.a_sh : &maps.b_sh;
+        const int shared_row = m_side ? p.a_sh_row : p.b_sh_row;
+        const uint32_t dst0 = smem_u32(tiles) + (m_side ? 0 : kWgABytes);
+        const uint32_t full0 = mapa_shared(smem_u32(full), 0), tail0 = mapa_shared(smem_u32(tail_full), rank);
         int stage = 0;
-        uint32_t phase = 0, armed = 0, armed_par = 0;
+        // last use of each stage with a load that completes here (bits by stage): on which barrier and parity
+        uint32_t phase = 0, armed = 0, on_tail = 0, full_par = 0, tail_par = 0;
         bool ok = true;
-        for (int i = 0; ok && i * W < total; ++i) {
-            const int u = snake_unit(i, blockIdx.x, W, total);
+        for (int i = 0; ok && i * npairs < total; ++i) {
+            const int u = snake_unit(i, pair, npairs, total);
             if (u < 0) continue;
             const WUnit w = unit_at(u);
-            const CUtensorMap* am = w.g < E ? &maps.a : &maps.a_sh;
-            const CUtensorMap* bm = w.g < E ? &maps.b : &maps.b_sh;
-            const int a_row = w.g < E ? offs[w.g] : p.a_sh_row, b_row = w.g < E ? offs[w.g] : p.b_sh_row;
-            const uint32_t tx = (uint32_t)(kWgABytes + w.ncols / 64 * kMnBoxBytes);
+            const CUtensorMap* map = w.g < E ? routed_map : shared_map;
+            const int row = w.g < E ? offs[w.g] : shared_row;
+            // first 64-column block: past M (zero fill) in the second CTA for an odd last block of M; for an odd
+            // last block of N each CTA uses one of the two it loads
+            const int blk = m_side ? w.mb * (kWgTile / 64) + 2 * rank : w.nb * (kWgTile / 64) + rank * (w.ncols / 128);
             for (int k = 0; k < w.rows; k += kWgKRows) {
+                const uint32_t bit = 1u << stage;
+                const bool tail = is_tail(w.rows, k);
                 ok = mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, p.err, abort_flag, true);
                 if (!ok) break;
-                const uint32_t fb = smem_u32(&full[stage]);
-                const uint32_t a_s = smem_u32(tiles + (size_t)stage * kWgStageBytes);
-                mbar_arrive_expect_tx(fb, tx);
-                for (int j = 0; j < 2; ++j)
-                    tma_load_2d(a_s + j * kMnBoxBytes, am, w.mb * 128 + 64 * j, a_row + k, fb, pol);
-                for (int j = 0; j < w.ncols / 64; ++j)
-                    tma_load_2d(a_s + kWgABytes + j * kMnBoxBytes, bm, w.nb * kWgN + 64 * j, b_row + k, fb, pol);
-                armed |= 1u << stage;
-                armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
+                if (m_side) {
+                    if (tail) {
+                        mbar_arrive_expect_tx(smem_u32(&tail_full[stage]), kWgStageBytes);
+                        tail_par ^= bit;
+                        on_tail |= bit;
+                        armed |= bit;
+                    } else if (rank == 0) {
+                        mbar_arrive_expect_tx(smem_u32(&full[stage]), 2 * kWgStageBytes);
+                        on_tail &= ~bit;
+                        armed |= bit;
+                    }
+                    full_par = (full_par & ~bit) | (phase << stage);
+                }
+                tma_load_3d_pair(dst0 + (uint32_t)stage * kWgStageBytes, map, 0, row + k, blk,
+                                 (tail ? tail0 : full0) + 8u * (uint32_t)stage, pol);
                 if (++stage == S) { stage = 0; phase ^= 1u; }
             }
         }
-        for (int s = 0; s < S; ++s)   // every load issued must land before the CTA may exit
-            if ((armed >> s) & 1u) mbar_wait(smem_u32(&full[s]), (armed_par >> s) & 1u, p.err, abort_flag, false);
-    } else if (warp == 1) {
-        // ---------------------------------------------------------------- MMA (lane 0; all lanes clear row tails)
-        const uint32_t idesc0 = idesc_bf16_f32(128, 0) | kIdescAMajorM | kIdescBMajorN;
-        int stage = 0, acc = 0;
-        uint32_t phase = 0, acc_phase = 0;
+        // every load that completes on a barrier of this CTA must land before the CTA may exit (an earlier
+        // use of a stage has landed when the stage was used again); the M side waits for both
+        for (int s = 0; s < S; ++s)
+            if ((armed >> s) & 1u) {
+                const bool t = (on_tail >> s) & 1u;
+                mbar_wait(smem_u32(t ? &tail_full[s] : &full[s]), t ? ((tail_par >> s) & 1u) ^ 1u : (full_par >> s) & 1u,
+                          p.err, abort_flag, false);
+            }
+    } else if (warp == 1 && rank == 0) {
+        // ---------------------------------------------------------------- MMA issuer (first CTA)
+        // The tensor cores take few MMAs ahead: whatever this warp does between one stage's MMAs and the
+        // next's beyond the 512 clocks that they run is lost, and a lone warp needs some 5 clocks an
+        // instruction. So its loop is one wait, four MMAs from two precomputed descriptors, one commit, with
+        // the warp converged and one lane elected (a single running lane measured 7% slower).
+        const uint32_t idesc0 = idesc_bf16_f32(256, 0) | kIdescAMajorM | kIdescBMajorN;
+        const uint64_t a0 = smem_desc_mnmajor(smem_u32(tiles), kMnBoxBytes);
+        const uint64_t b0 = smem_desc_mnmajor(smem_u32(tiles) + kWgABytes, kMnBoxBytes);
+        const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty), tfull0 = smem_u32(tfull), tempty0 = smem_u32(tempty);
+        int stage = 0;
+        uint32_t phase = 0, acc = 0, acc_phase = 1;
         bool ok = true;
-        for (int i = 0; ok && i * W < total; ++i) {
-            const int u = snake_unit(i, blockIdx.x, W, total);
+        for (int i = 0; ok && i * npairs < total; ++i) {
+            const int u = snake_unit(i, pair, npairs, total);
             if (u < 0) continue;
             const WUnit w = unit_at(u);
             const uint32_t idesc = idesc0 | ((uint32_t)(w.ncols >> 3) << 17);
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&tempty[acc]), acc_phase ^ 1u, p.err, abort_flag, true));
+            const uint32_t d = tmem_base + acc * kWgTile;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(tempty0 + 8 * acc, acc_phase, p.err, abort_flag, true));
             if (!ok) break;
             tc_fence_after();
-            const uint32_t d = tmem_base + (uint32_t)(acc * kWgN);
-            for (int k = 0; k < w.rows; k += kWgKRows) {
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&full[stage]), phase, p.err, abort_flag, true));
+            uint32_t accum = 0;
+            for (int left = w.rows; left > 0; left -= kWgKRows) {
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(full0 + 8 * stage, phase, p.err, abort_flag, true));
                 if (!ok) break;
-                uint8_t* st = tiles + (size_t)stage * kWgStageBytes;
-                const int valid = min(kWgKRows, w.rows - k), ksteps = (valid + 15) / 16;
-                if (valid & 15) {
-                    // rows valid .. 16 ksteps - 1 of every box: whole 128-byte lines, whatever the swizzle
-                    const int n = 8 * (16 * ksteps - valid), boxes = 2 + w.ncols / 64;
-                    for (int z = lane; z < n * boxes; z += 32)
-                        *reinterpret_cast<uint4*>(st + (z / n) * kMnBoxBytes + valid * 128 + (z % n) * 16) =
-                            make_uint4(0u, 0u, 0u, 0u);
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                }
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t a_s = smem_u32(st), b_s = a_s + kWgABytes;
-                    for (int kk = 0; kk < ksteps; ++kk)
-                        umma_f16_ss(d, smem_desc_mnmajor(a_s + kk * kMnKStep, kMnBoxBytes),
-                                    smem_desc_mnmajor(b_s + kk * kMnKStep, kMnBoxBytes), idesc, (k | kk) != 0 ? 1u : 0u);
-                    umma_commit(smem_u32(&empty[stage]));
+                const uint64_t a = a0 + (uint32_t)stage * (kWgStageBytes >> 4), b = b0 + (uint32_t)stage * (kWgStageBytes >> 4);
+                if (elect_one()) {
+                    umma_f16_ss_pair(d, a, b, idesc, accum);
+                    if (left > 16) umma_f16_ss_pair(d, a + (kMnKStep >> 4), b + (kMnKStep >> 4), idesc, 1u);
+                    if (left > 32) umma_f16_ss_pair(d, a + 2 * (kMnKStep >> 4), b + 2 * (kMnKStep >> 4), idesc, 1u);
+                    if (left > 48) umma_f16_ss_pair(d, a + 3 * (kMnKStep >> 4), b + 3 * (kMnKStep >> 4), idesc, 1u);
+                    umma_commit_pair_both(empty0 + 8 * stage);
                 }
                 __syncwarp();
+                accum = 1;
                 if (++stage == S) { stage = 0; phase ^= 1u; }
             }
             if (!ok) break;
-            if (lane == 0) umma_commit(smem_u32(&tfull[acc]));
+            if (elect_one()) umma_commit_pair_both(tfull0 + 8 * acc);
             __syncwarp();
-            acc ^= 1;
+            acc ^= 1u;
             if (acc == 0) acc_phase ^= 1u;
         }
-        if (lane == 0) {   // all MMAs issued must finish before TMEM is released
-            umma_commit(smem_u32(drain));
+        // all MMAs issued must finish before TMEM is released
+        if (elect_one()) {
+            umma_commit_pair(mapa_shared(smem_u32(drain), 0));
             mbar_wait(smem_u32(drain), 0u, p.err, abort_flag, false);
         }
         __syncwarp();
-    } else if (warp >= 2) {
+    } else if (warp == 2) {
+        // ---------------------------------------------------------------- row tails (both CTAs)
+        int stage = 0;
+        uint32_t tail_par = 0;
+        bool ok = true;
+        for (int i = 0; ok && i * npairs < total; ++i) {
+            const int u = snake_unit(i, pair, npairs, total);
+            if (u < 0) continue;
+            const WUnit w = unit_at(u);
+            const int stages = (w.rows + kWgKRows - 1) / kWgKRows;
+            if (stages == 0) continue;
+            const int last = (stage + stages - 1) % S, valid = w.rows - (stages - 1) * kWgKRows;
+            stage = (stage + stages) % S;
+            if ((valid & 15) == 0) continue;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&tail_full[last]), (tail_par >> last) & 1u, p.err, abort_flag, true));
+            if (!ok) break;
+            tail_par ^= 1u << last;
+            // rows valid .. up to the next multiple of 16: whole 128-byte lines of every box, whatever the swizzle
+            uint8_t* st = tiles + (size_t)last * kWgStageBytes + (lane & 7) * 16;
+            const int end = (valid + 15) & ~15, boxes = 2 + w.ncols / 128;
+            for (int r = valid + (lane >> 3); r < end; r += 4)
+                for (int z = 0; z < boxes; ++z)
+                    *reinterpret_cast<uint4*>(st + z * kMnBoxBytes + r * 128) = make_uint4(0u, 0u, 0u, 0u);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // for the tensor cores
+            __syncwarp();
+            if (rank != 0) {
+                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tail_ready[last]), 0));
+            } else {
+                const uint32_t bar = smem_u32(&tail_ready[last]), par = ((tail_par >> last) & 1u) ^ 1u;
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar, par, p.err, abort_flag, true));
+                if (!ok) break;
+                if (lane == 0) mbar_arrive(smem_u32(&full[last]));
+            }
+        }
+    } else if (warp >= 4) {
         // ---------------------------------------------------------------- epilogue: TMEM -> bf16 -> TMA store
-        const int q = warp & 3;
-        uint8_t* stg = staging + q * kWgStoreBytes;
+        constexpr int G = kWgEpiWarps / 4;
+        const int q = warp & 3, g0 = (warp - 4) >> 2;
+        uint8_t* const stg0 = staging + (warp - 4) * 2 * kWgStoreBytes;
+        int buf = 0;
         const uint64_t pol = l2_policy_evict_first();
         int acc = 0;
         uint32_t acc_phase = 0;
-        for (int i = 0; i * W < total; ++i) {
-            const int u = snake_unit(i, blockIdx.x, W, total);
+        for (int i = 0; i * npairs < total; ++i) {
+            const int u = snake_unit(i, pair, npairs, total);
             if (u < 0) continue;
             const WUnit w = unit_at(u);
-            const int m = w.mb * 128 + q * 32;
+            const int m = w.mb * kWgTile + rank * 128 + q * 32;
             const int part = m >= p.m_split ? 1 : 0;
             const CUtensorMap* om = w.g < E ? &maps.out[part] : &maps.out_sh[part];
             const int y = (w.g < E ? w.g * p.m_split : 0) + m - part * p.m_split;
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&tfull[acc]), acc_phase, p.err, abort_flag, true))) break;
             tc_fence_after();
-            const uint32_t t_row = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kWgN);
-            for (int c = 0; c < w.ncols; c += 64) {
-                uint32_t v[32];
+            const uint32_t t_row = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kWgTile);
+            // the warp's boxes (64-column boxes g0, g0 + G, ..) into registers first, so that the accumulator
+            // goes back before the stores
+            constexpr int NBOX = kWgTile / 64 / G;
+            uint32_t v[NBOX][32];
+#pragma unroll
+            for (int b = 0; b < NBOX; ++b) {
+                const int c = 64 * (g0 + G * b);
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
                     uint32_t a[32];
-                    if (w.rows > 0) {
+                    if (w.rows > 0 && c < w.ncols) {
                         tmem_ld_x32_wait(t_row + c + 32 * z, a);
                     } else {
 #pragma unroll
@@ -243,24 +366,30 @@ expert_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradParams p)
                     }
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
-                        v[16 * z + j] = pack_bf16x2(__uint_as_float(a[2 * j]), __uint_as_float(a[2 * j + 1]));
+                        v[b][16 * z + j] = pack_bf16x2(__uint_as_float(a[2 * j]), __uint_as_float(a[2 * j + 1]));
                 }
-                if (c + 64 >= w.ncols) {   // all of this warp's accumulator has been read
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&tempty[acc]));
-                }
-                // the previous box has left the staging buffer
-                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            }
+            // a relaxed arrive (tcgen05.wait::ld has completed every load), as in expert_gemm_pair_kernel
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&tempty[acc]), 0));
+#pragma unroll
+            for (int b = 0; b < NBOX; ++b) {
+                const int c = 64 * (g0 + G * b);
+                if (c >= w.ncols || m >= p.M) break;
+                // the store before the last has left this staging buffer
+                uint8_t* stg = stg0 + buf * kWgStoreBytes;
+                buf ^= 1;
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
                 __syncwarp();
 #pragma unroll
                 for (int x = 0; x < 8; ++x)   // the 128-byte swizzle: 16-byte chunk x of row l lies at x ^ (l & 7)
                     *reinterpret_cast<uint4*>(stg + lane * 128 + ((x ^ (lane & 7)) << 4)) =
-                        make_uint4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+                        make_uint4(v[b][4 * x], v[b][4 * x + 1], v[b][4 * x + 2], v[b][4 * x + 3]);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) {
-                    tma_store_2d(om, w.nb * kWgN + c, y, smem_u32(stg), pol);
+                    tma_store_2d(om, w.nb * kWgTile + c, y, smem_u32(stg), pol);
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 }
             }
@@ -273,18 +402,36 @@ expert_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradParams p)
 
     tc_fence_before();
     __syncthreads();
+    if (*abort_flag) __nanosleep(100000);   // give loads still in flight after a timeout time to land
+    cluster_sync();   // the peer's shared memory and TMEM stay alive until the pair's MMAs are done
     if (warp == 0) {
         tc_fence_after();
-        tmem_dealloc(tmem_base, kTmemCols);
+        tmem_dealloc_pair(tmem_base, kTmemCols);
     }
 }
 
-cudaError_t run_wgrad(const WgradMaps& maps, const WgradParams& p, KernelId id, int num_sms, cudaStream_t s) {
-    const size_t smem = wgrad_smem_bytes(p.E);
+cudaError_t run_wgrad(const WgradMaps& maps, WgradParams p, KernelId id, int num_sms, cudaStream_t s) {
+    p.stages = kWgMaxStages;
+    while (p.stages > 2 && wgrad_smem_bytes(p.stages, p.E) > (size_t)max_dynamic_smem()) --p.stages;
+    const uint64_t nb = (uint64_t)((p.N + kWgTile - 1) / kWgTile), upg = nb * ((p.M + kWgTile - 1) / kWgTile);
+    p.inv_nb = (uint32_t)(((1ull << 32) + nb - 1) / nb);   // 0 for 1, which is not divided by
+    p.inv_upg = (uint32_t)(((1ull << 32) + upg - 1) / upg);
+    const size_t smem = wgrad_smem_bytes(p.stages, p.E);
     cudaError_t e = cudaFuncSetAttribute(expert_wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
+    static int max_clusters = 0;   // pairs resident at once
+    if (max_clusters == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(num_sms & ~1);
+        cfg.blockDim = dim3(kWgThreads);
+        cfg.dynamicSmemBytes = smem;
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, expert_wgrad_kernel, &cfg);
+        if (e != cudaSuccess) return e;
+        max_clusters = n > 0 ? n : 1;
+    }
     LaunchTimer lt(id, s);
-    return launch_pdl(expert_wgrad_kernel, dim3(num_sms), dim3(kWgThreads), smem, s, maps, p);
+    return launch_pdl(expert_wgrad_kernel, dim3(2 * std::min(num_sms / 2, max_clusters)), dim3(kWgThreads), smem, s, maps, p);
 }
 
 }  // namespace
@@ -309,11 +456,11 @@ cudaError_t launch_expert_ffn_backward(const smoe_config_t& c, const ExpertBackw
         !act_maps(m1.sh, b.dout, T, H) ||
         !make_map(&m2.w, wgu, (uint64_t)(E + 1) * 2 * I * (H / 64), 64, 64, BK) ||
         !act_maps(m2.act, b.dgu, rows, 2 * I) ||
-        !make_map(&wd.a, b.dy, routed, H, 64, BK) || !make_map(&wd.a_sh, b.dout, T, H, 64, BK) ||
-        !make_map(&wd.b, b.h, rows, I, 64, BK) || !make_map(&wd.out[0], b.dw_down, (uint64_t)E * H, I, 32, BK) ||
+        !make_wgrad_map(&wd.a, b.dy, routed, H) || !make_wgrad_map(&wd.a_sh, b.dout, T, H) ||
+        !make_wgrad_map(&wd.b, b.h, rows, I) || !make_map(&wd.out[0], b.dw_down, (uint64_t)E * H, I, 32, BK) ||
         !make_map(&wd.out_sh[0], b.dws_down, H, I, 32, BK) ||
-        !make_map(&wg.a, b.dgu, rows, 2 * I, 64, BK) || !make_map(&wg.b, b.x_perm, routed, H, 64, BK) ||
-        !make_map(&wg.b_sh, b.x, T, H, 64, BK) ||
+        !make_wgrad_map(&wg.a, b.dgu, rows, 2 * I) || !make_wgrad_map(&wg.b, b.x_perm, routed, H) ||
+        !make_wgrad_map(&wg.b_sh, b.x, T, H) ||
         !make_map(&wg.out[0], b.dw_gate, (uint64_t)E * I, H, 32, BK) ||
         !make_map(&wg.out[1], b.dw_up, (uint64_t)E * I, H, 32, BK) ||
         !make_map(&wg.out_sh[0], b.dws_gate, I, H, 32, BK) || !make_map(&wg.out_sh[1], b.dws_up, I, H, 32, BK))
@@ -336,10 +483,10 @@ cudaError_t launch_expert_ffn_backward(const smoe_config_t& c, const ExpertBackw
                   1, 0, b.dx_rows, nullptr, err};
     e = pairs ? run_gemm_pair<MODE_DX>(m2, p2, num_sms, s) : run_gemm<MODE_DX>(m2, p2, num_sms, s);
     if (e != cudaSuccess) return e;
-    e = run_wgrad(wg, WgradParams{b.offsets, E, (int)T, (int)routed, 2 * I, H, I, (int)routed, 0, err},
+    e = run_wgrad(wg, WgradParams{b.offsets, E, (int)T, (int)routed, 2 * I, H, I, (int)routed, 0, 0, 0, 0, err},
                   K_EXPERT_WGRAD_GATEUP, num_sms, s);
     if (e != cudaSuccess) return e;
-    e = run_wgrad(wd, WgradParams{b.offsets, E, (int)T, (int)routed, H, I, H, 0, (int)routed, err},
+    e = run_wgrad(wd, WgradParams{b.offsets, E, (int)T, (int)routed, H, I, H, 0, (int)routed, 0, 0, 0, err},
                   K_EXPERT_WGRAD_DOWN, num_sms, s);
     if (e == cudaSuccess) launches_add(4);
     return e;

@@ -264,8 +264,8 @@ def test_expert_ffn_save(name, gather):
 
 
 def test_checkpoint_of_extreme_products():
-    """Products that are 0, infinite or NaN in one feature: their row's other blocks are unaffected, and in
-    their own block they do not move the scale."""
+    """Products that are 0, infinite or NaN in one feature: infinite and NaN products are held as such in a
+    block of scale 2^120, the row's other blocks are unaffected."""
     name = "tiny"
     T, H, E, k, I, _, _ = SHAPES[name]
     rng = np.random.default_rng(22)
@@ -286,13 +286,17 @@ def test_checkpoint_of_extreme_products():
     smoe.smoe_expert_ffn_save(cfg, x, x_perm, _i32(r["row_token"]), _i32(r["offsets"]), T, packed, y, q, sc, _ws(cfg, T))
     exps = sc.cpu().numpy()
     held = ob.checkpoint_values(q.cpu().numpy(), exps)
-    assert np.isnan(held[:, 5]).all() and np.isnan(held[:, I + 70]).all()
-    assert (exps[1] == 127).all() and not held[:, 32:64].any()
+    # an infinity has the exponent of 448 * 2^120, NaN's all-ones mantissa carries into the next; 448 * 2^120 is
+    # infinite in fp32, which is what the values are read as (as is inf - inf = NaN)
+    assert not np.isfinite(held[:, 5].astype(np.float32)).any() and np.isnan(held[:, I + 70]).all()
+    assert np.isin(exps[[0, I // 32 + 2]], (247, 248)).all()
+    assert (exps[1] == 1).all() and not held[:, 32:64].any()
     b = _bounds(r, T, k)
     for e in range(E + 1):
         X = rows64[b[e]:b[e + 1]]
         W = np.concatenate([g64[e], u64[e]])
         fine = np.isfinite(W).all(1)
+        fine[0:32] = fine[I + 64:I + 96] = False      # the blocks of the infinite and the NaN feature
         ref = X @ np.where(fine[:, None], W, 0.0).T
         err = 2 * H * F * (np.abs(X) @ np.abs(np.where(fine[:, None], W, 0.0)).T)
         scale = np.repeat(np.exp2(exps.T[b[e]:b[e + 1]].astype(float) - 127), 32, axis=1)

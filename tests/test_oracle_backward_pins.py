@@ -95,7 +95,7 @@ def test_checkpoint_holds_values_to_half_a_step():
     held, exps = ob.checkpoint(v)
     scale = np.repeat(np.exp2(exps.T.astype(float) - 127), 32, axis=1)
     assert (np.abs(held - v) <= np.maximum(np.abs(v) * 2.0 ** -4, scale * 2.0 ** -10)).all()
-    assert exps[0, 3] == 127 and exps[0, 4] == 127 + 9 and exps[0, 5] == 128
+    assert exps[0, 3] == 1 and exps[0, 4] == 127 + 9 and exps[0, 5] == 128
     top = np.abs(v).reshape(64, 4, 32).max(axis=2).T
     some = top > 0
     assert (top <= 448.0 * np.exp2(exps.astype(float) - 127)).all()
