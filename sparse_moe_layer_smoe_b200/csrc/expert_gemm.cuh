@@ -1038,9 +1038,17 @@ expert_gemm_pair_kernel(const __grid_constant__ GemmMaps maps, const GemmParams 
                     mbar_wait(smem_u32(&full[s]), (armed_par >> s) & 1u, p.err, abort_flag, false);
         }
         __syncwarp(pmask);
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0) {
         // ---------------------------------------------------------------- MMA issuer (first CTA)
+        // The tensor cores take few MMAs ahead, so the time this warp spends between one stage's MMAs and
+        // the next's is partly lost: descriptors are precomputed and stepped, one multicast commit frees
+        // the stage in both CTAs, and the warp stays converged with one lane elected to issue.
         const uint32_t idesc0 = (F8 ? idesc_e4m3_f32(256, 0) : idesc_bf16_f32(256, 0)) | (mode_mn<MODE>() ? kIdescAMajorM : 0u);
+        const uint64_t a0 = mode_mn<MODE>() ? smem_desc_mnmajor(smem_u32(tiles), kMnBoxBytes)
+                                            : smem_desc_kmajor<C::SW>(smem_u32(tiles));
+        const uint64_t b0 = smem_desc_kmajor<C::SW>(smem_u32(tiles) + C::A_BYTES);
+        constexpr uint32_t a_step = (mode_mn<MODE>() ? kMnKStep : 32u) >> 4, b_step = 32u >> 4;
+        const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty), tfull0 = smem_u32(tfull), tempty0 = smem_u32(tempty);
         int stage = 0, acc = 0;
         uint32_t phase = 0, acc_phase = 0;
         bool ok = true;
@@ -1050,41 +1058,41 @@ expert_gemm_pair_kernel(const __grid_constant__ GemmMaps maps, const GemmParams 
             const Unit w = decode_unit(u, MBP, ttab, offs, E, p.T, p.nt_max);
             const int n_mma = mma_cols(group_rows(w.g, E, p.T, offs) - w.nb * w.nt, w.nt);
             const uint32_t idesc = idesc0 | ((uint32_t)(n_mma >> 3) << 17);
-            if (!mbar_wait(smem_u32(&tempty[acc]), acc_phase ^ 1u, p.err, abort_flag, true)) break;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(tempty0 + 8 * acc, acc_phase ^ 1u, p.err, abort_flag, true));
+            if (!ok) break;
             tc_fence_after();
             const uint32_t d = tmem_base + (uint32_t)(acc * ACC_COLS);
+            uint32_t accum = 0;
             for (int kb = 0; kb < KB; ++kb) {
-                if (!mbar_wait(smem_u32(&full[stage]), phase, p.err, abort_flag, true)) { ok = false; break; }
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(full0 + 8 * stage, phase, p.err, abort_flag, true));
+                if (!ok) break;
                 tc_fence_after();
-                const uint32_t a_s = smem_u32(tiles + (size_t)stage * STAGE_B);
-                const uint32_t b_s = a_s + C::A_BYTES;
+                const uint64_t a = a0 + (uint32_t)(stage * STAGE_B >> 4), b = b0 + (uint32_t)(stage * STAGE_B >> 4);
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < BK / 16; ++kk) {
-                    const uint32_t accum = (kb | kk) != 0 ? 1u : 0u;
-                    const uint64_t bdesc = smem_desc_kmajor<C::SW>(b_s + kk * 32);
-                    const uint64_t adesc = mode_mn<MODE>() ? smem_desc_mnmajor(a_s + kk * kMnKStep, kMnBoxBytes)
-                                                           : smem_desc_kmajor<C::SW>(a_s + kk * 32);
-                    if (F8)
-                        umma_f8_ss_pair(d, adesc, bdesc, idesc, accum);
-                    else
-                        umma_f16_ss_pair(d, adesc, bdesc, idesc, accum);
-                    if (DUAL) {
-                        const uint64_t udesc = smem_desc_kmajor<C::SW>(a_s + C::UP_OFFSET + kk * 32);
+                    for (int kk = 0; kk < BK / 16; ++kk) {
+                        const uint32_t on = kk == 0 ? accum : 1u;
                         if (F8)
-                            umma_f8_ss_pair(d + p.nt_max, udesc, bdesc, idesc, accum);
+                            umma_f8_ss_pair(d, a + kk * a_step, b + kk * b_step, idesc, on);
                         else
-                            umma_f16_ss_pair(d + p.nt_max, udesc, bdesc, idesc, accum);
+                            umma_f16_ss_pair(d, a + kk * a_step, b + kk * b_step, idesc, on);
+                        if (DUAL) {
+                            constexpr uint32_t up = C::UP_OFFSET >> 4;
+                            if (F8)
+                                umma_f8_ss_pair(d + p.nt_max, a + up + kk * a_step, b + kk * b_step, idesc, on);
+                            else
+                                umma_f16_ss_pair(d + p.nt_max, a + up + kk * a_step, b + kk * b_step, idesc, on);
+                        }
                     }
+                    umma_commit_pair_both(empty0 + 8 * stage);
                 }
-                const uint32_t eb = smem_u32(&empty[stage]);
-                umma_commit_pair(mapa_shared(eb, 0));
-                umma_commit_pair(mapa_shared(eb, 1));
+                __syncwarp();
+                accum = 1;
                 if (++stage == S) { stage = 0; phase ^= 1u; }
             }
             if (!ok) break;
-            const uint32_t tb = smem_u32(&tfull[acc]);
-            umma_commit_pair(mapa_shared(tb, 0));
-            umma_commit_pair(mapa_shared(tb, 1));
+            if (elect_one()) umma_commit_pair_both(tfull0 + 8 * acc);
+            __syncwarp();
             if (NACC == 2) {
                 acc ^= 1;
                 if (acc == 0) acc_phase ^= 1u;
@@ -1092,8 +1100,11 @@ expert_gemm_pair_kernel(const __grid_constant__ GemmMaps maps, const GemmParams 
                 acc_phase ^= 1u;
             }
         }
-        umma_commit_pair(mapa_shared(smem_u32(drain), 0));
-        mbar_wait(smem_u32(drain), 0u, p.err, abort_flag, false);
+        if (elect_one()) {
+            umma_commit_pair(mapa_shared(smem_u32(drain), 0));
+            mbar_wait(smem_u32(drain), 0u, p.err, abort_flag, false);
+        }
+        __syncwarp();
     } else if (warp >= 2) {
         // ---------------------------------------------------------------- epilogue (both CTAs)
         // warp w reads TMEM lanes 32 (w % 4)..+31; with G = 1, 2 or 4 epilogue warps per lane
