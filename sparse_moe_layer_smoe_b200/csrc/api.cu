@@ -40,7 +40,7 @@ const char* const kNames[K_NUM_KERNELS] = {"router_logits", "router_topk",   "pe
                                            "quantize_h",    "pack_fp8",    "expert_gateup_save",
                                            "expert_dh",     "expert_dx",   "expert_wgrad_down",
                                            "expert_wgrad_gateup", "checkpoint_values", "combine_backward",
-                                           "permute_backward", "router_dlogits", "router_wgrad",
+                                           "permute_backward", "router_backward",
                                            "router_wgrad_join"};
 }  // namespace
 
@@ -524,7 +524,6 @@ smoe_status_t smoe_route_backward(const smoe_config_t* c, const smoe_bf16_t* x, 
     SMOE_TRY(check_ws_backward(c, T, ws, ws_bytes));
     const BwdLayout L = bwd_layout(*c, T);
     const RouteBackward b{x, logits, topk_idx, topk_w, dtopk_w, offsets, perm_row, row_token, dlogits, dw_router,
-                          at<float>(ws, L.dl_row), at<int4>(ws, L.items), at<int32_t>(ws, L.n_items),
                           at<float>(ws, L.partial)};
     return cuda_status(launch_route_backward(*c, b, T, at<int32_t>(ws, L.err), static_cast<cudaStream_t>(stream)));
 }

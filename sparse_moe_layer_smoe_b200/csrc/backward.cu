@@ -34,9 +34,12 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 
 constexpr int kSlots = 8;      // slots a pass over a token's row takes (top-k 8; a larger k takes several passes)
 constexpr int kMaxWarps = 8;
+constexpr int kAhead = 2;      // router rows in flight beside the routed ones (1, 2 and 4 measure the same)
 
-// One CTA per token; a thread owns 8 consecutive features of every row.
-__global__ void __launch_bounds__(256) combine_backward_kernel(const uint16_t* __restrict__ dout,
+// One CTA per token; a thread owns 8 consecutive features of every row and has all k of them in flight.
+// HBM-bound: 8192 tokens of H = 4096, k = 8 in 186 us, 6.1 TB/s (two CTAs an SM instead of three: 199 us;
+// four spill: 241 us).
+__global__ void __launch_bounds__(256, 3) combine_backward_kernel(const uint16_t* __restrict__ dout,
                                                                const uint16_t* __restrict__ y,
                                                                const int32_t* __restrict__ perm_row,
                                                                const float* __restrict__ topk_w, int T, int k, int H,
@@ -105,8 +108,12 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const uint16_t* _
     }
 }
 
-// One CTA per token. The router's term is left out when dlogits is null.
-__global__ void __launch_bounds__(256) permute_backward_kernel(const uint16_t* __restrict__ dx_rows,
+// One CTA per token. The router's term is left out when dlogits is null. With it a token reads 16 KB of the
+// router's weights for each of its experts (at H = 4096), more than the rows themselves, but from L2: 8192
+// tokens take 129 us, 5.2 TB/s of HBM beside as much again and half from L2. Four CTAs an SM matter (three:
+// 139 us, two: 163). Keeping the weights of a 128-feature slice of all experts in shared memory, so that
+// only the rows cross L2, was slower: 228 us, as rows are then read in 256-byte pieces.
+__global__ void __launch_bounds__(256, 4) permute_backward_kernel(const uint16_t* __restrict__ dx_rows,
                                                                const int32_t* __restrict__ perm_row,
                                                                const int32_t* __restrict__ topk_idx,
                                                                const float* __restrict__ dlogits,
@@ -119,20 +126,23 @@ __global__ void __launch_bounds__(256) permute_backward_kernel(const uint16_t* _
     const int t = blockIdx.x;
     const int vec = H / 8;
     const int64_t nrouted = (int64_t)T * k;
-    if ((int)threadIdx.x < k) {
+    if (threadIdx.x < 32) {
         const size_t i = (size_t)t * k + threadIdx.x;
-        int32_t r = perm_row[i], e = -1;
+        int32_t r = -1, e = 0;
         float g = 0.f;
-        if (r < 0 || r >= nrouted) {
+        const bool entry = (int)threadIdx.x < k;
+        if (entry) r = perm_row[i];
+        if (entry && (r < 0 || r >= nrouted)) {
             record_error(err, SMOE_ERR_DEVICE);
             r = -1;
         }
-        if (dlogits != nullptr) {
+        if (entry && dlogits != nullptr) {
             e = topk_idx[i];
             g = dlogits[i];
             if (e < 0 || e >= E) {
                 record_error(err, SMOE_ERR_DEVICE);
-                e = -1;
+                e = 0;
+                g = 0.f;
             }
         }
         rows[threadIdx.x] = r;
@@ -140,159 +150,165 @@ __global__ void __launch_bounds__(256) permute_backward_kernel(const uint16_t* _
         dl[threadIdx.x] = g;
     }
     __syncthreads();
+    const bool router = dlogits != nullptr;
     for (int c = threadIdx.x; c < vec; c += blockDim.x) {
         float acc[8];
         unpack8(reinterpret_cast<const uint4*>(dx_rows)[(size_t)(nrouted + t) * vec + c], acc);
         for (int j0 = 0; j0 < k; j0 += kSlots) {
+            // the rows and the first router weights in flight together, then the rest of the weights
             uint4 v[kSlots];
 #pragma unroll
-            for (int j = 0; j < kSlots; ++j)
-                if (j0 + j < k && rows[j0 + j] >= 0)
-                    v[j] = reinterpret_cast<const uint4*>(dx_rows)[(size_t)rows[j0 + j] * vec + c];
-#pragma unroll
-            for (int j = 0; j < kSlots; ++j)
-                if (j0 + j < k && rows[j0 + j] >= 0) {
-                    float f[8];
-                    unpack8(v[j], f);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) acc[i] += f[i];
-                }
-        }
-        for (int j = 0; j < k; ++j)
-            if (experts[j] >= 0) {
-                const float4* w4 = reinterpret_cast<const float4*>(w_router + (size_t)experts[j] * H) + 2 * c;
-                const float4 a = w4[0], b = w4[1];
-                const float g = dl[j];
-                acc[0] = fmaf(g, a.x, acc[0]);
-                acc[1] = fmaf(g, a.y, acc[1]);
-                acc[2] = fmaf(g, a.z, acc[2]);
-                acc[3] = fmaf(g, a.w, acc[3]);
-                acc[4] = fmaf(g, b.x, acc[4]);
-                acc[5] = fmaf(g, b.y, acc[5]);
-                acc[6] = fmaf(g, b.z, acc[6]);
-                acc[7] = fmaf(g, b.w, acc[7]);
+            for (int j = 0; j < kSlots; ++j) {
+                v[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (rows[j0 + j] >= 0) v[j] = reinterpret_cast<const uint4*>(dx_rows)[(size_t)rows[j0 + j] * vec + c];
             }
+#pragma unroll
+            for (int z = 0; z < kSlots; z += kAhead) {
+                float4 a[kAhead], b[kAhead];
+                if (router) {
+#pragma unroll
+                    for (int j = 0; j < kAhead; ++j) {
+                        // a skipped entry has weight 0 on expert 0's row
+                        const float4* w4 = reinterpret_cast<const float4*>(w_router + (size_t)experts[j0 + z + j] * H) + 2 * c;
+                        a[j] = w4[0];
+                        b[j] = w4[1];
+                    }
+                }
+                if (z == 0) {
+#pragma unroll
+                    for (int j = 0; j < kSlots; ++j) {
+                        float f[8];
+                        unpack8(v[j], f);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) acc[i] += f[i];
+                    }
+                }
+                if (router) {
+#pragma unroll
+                    for (int j = 0; j < kAhead; ++j) {
+                        const float g = dl[j0 + z + j];
+                        acc[0] = fmaf(g, a[j].x, acc[0]);
+                        acc[1] = fmaf(g, a[j].y, acc[1]);
+                        acc[2] = fmaf(g, a[j].z, acc[2]);
+                        acc[3] = fmaf(g, a[j].w, acc[3]);
+                        acc[4] = fmaf(g, b[j].x, acc[4]);
+                        acc[5] = fmaf(g, b[j].y, acc[5]);
+                        acc[6] = fmaf(g, b[j].z, acc[6]);
+                        acc[7] = fmaf(g, b[j].w, acc[7]);
+                    }
+                }
+            }
+        }
         reinterpret_cast<uint4*>(dx)[(size_t)t * vec + c] = pack8(acc);
     }
 }
 
-// Entry (t, j) per thread: dlogits, and the same value in row order for the weight gradient. The last
-// block lists the items of the weight gradient instead: every expert's rows in pieces of
-// kRouterItemRows (an expert without rows has one empty item, which writes its zeros).
-__global__ void __launch_bounds__(1024) router_dlogits_kernel(const float* __restrict__ logits,
-                                                             const int32_t* __restrict__ topk_idx,
-                                                             const float* __restrict__ topk_w,
-                                                             const float* __restrict__ dtopk_w,
-                                                             const int32_t* __restrict__ offsets,
-                                                             const int32_t* __restrict__ perm_row, int T, int k, int E,
-                                                             float inv_c, float* __restrict__ dlogits,
-                                                             float* __restrict__ dl_row, int4* __restrict__ items,
-                                                             int32_t* __restrict__ first_item, int32_t* err) {
+// dl of entry i = t * k + j, whose selected logit is l.
+__device__ __forceinline__ float dlogit(const float* __restrict__ w, const float* __restrict__ dw, int64_t t, int j, int k,
+                                        float l, float inv_c) {
+    const float dwj = dw[t * k + j];
+    float sum = 0.f;
+    for (int q = 0; q < k; ++q) sum = fmaf(w[t * k + q] * inv_c, dwj - dw[t * k + q], sum);
+    return w[t * k + j] * (1.0f / (1.0f + expf(l))) * sum;   // 1 / (1 + e^l) = 1 - sigmoid(l)
+}
+
+constexpr int kRbThreads = 128;   // 8 features a thread: 1024 features a CTA
+
+// One launch for both gradients. Item = up to kRouterItemRows rows of one expert (an expert without rows
+// has one empty item, which writes its zeros). CTA (x, y): for x below the item bound, item x's sum over
+// its rows in order, for the 1024 features of slice y; it works out its item from the offsets and its
+// rows' dl from the tokens' weights itself, so nothing has to run before it. Above the bound (y = 0):
+// dlogits of 128 entries each. An expert of one item writes dW_r, the others' items partial sums. Rows
+// are gathered from x in L2 (each is read by k experts), 8 in flight a thread; more and smaller items
+// (64 rows) instead of 256 halved the time of a skewed batch, whose long sums otherwise run alone.
+__global__ void __launch_bounds__(kRbThreads) router_backward_kernel(
+    const uint16_t* __restrict__ x, const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
+    const float* __restrict__ topk_w, const float* __restrict__ dtopk_w, const int32_t* __restrict__ offsets,
+    const int32_t* __restrict__ perm_row, const int32_t* __restrict__ row_token, int T, int k, int E, int H, float inv_c,
+    int max_items, float* __restrict__ dlogits, float* __restrict__ partial, float* __restrict__ dw_router, int32_t* err) {
+    __shared__ int32_t tok[kRouterItemRows];
+    __shared__ float g[kRouterItemRows];
+    __shared__ int32_t warp_tot[kRbThreads / 32];
+    __shared__ int4 found;   // expert, first row, rows, items of the expert
     pdl_wait();
     pdl_launch_dependents();
     const int64_t nrouted = (int64_t)T * k;
-    if (blockIdx.x == gridDim.x - 1) {
-        __shared__ int32_t warp_tot[32];
-        __shared__ int bad;
-        const int e = threadIdx.x, lane = e & 31, w = e >> 5;
-        if (e == 0) bad = 0;
-        __syncthreads();
-        int32_t r0 = 0, r1 = 0;
-        if (e < E) {
-            r0 = offsets[e];
-            r1 = offsets[e + 1];
-            if (r0 < 0 || r1 < r0 || r1 > nrouted) bad = 1;
+    if ((int)blockIdx.x >= max_items) {
+        const int64_t i = (int64_t)(blockIdx.x - max_items) * kRbThreads + threadIdx.x;
+        if (blockIdx.y != 0 || i >= nrouted) return;
+        const int64_t t = i / k;
+        const int32_t e = topk_idx[i], r = perm_row[i];
+        if (e < 0 || e >= E || r < 0 || r >= nrouted) record_error(err, SMOE_ERR_DEVICE);
+        dlogits[i] = e >= 0 && e < E ? dlogit(topk_w, dtopk_w, t, (int)(i % k), k, logits[t * E + e], inv_c) : 0.f;
+        return;
+    }
+    // find the item: a scan of the experts' item counts, each thread a contiguous range of experts
+    {
+        const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+        const int chunk = (E + kRbThreads - 1) / kRbThreads, e0 = min((int)threadIdx.x * chunk, E), e1 = min(e0 + chunk, E);
+        bool bad = false;
+        int n = 0;
+        for (int e = e0; e < e1; ++e) {
+            const int a = offsets[e], b = offsets[e + 1];
+            bad |= a < 0 || b < a || b > nrouted;
+            n += max(1, (b - a + kRouterItemRows - 1) / kRouterItemRows);
         }
-        __syncthreads();
-        if (bad) {   // corrupt offsets: no rows
-            r0 = r1 = 0;
-            if (e == 0) record_error(err, SMOE_ERR_DEVICE);
+        bad = __syncthreads_or(bad);   // corrupt offsets: no rows, one empty item each
+        if (bad) {
+            n = e1 - e0;
+            if (threadIdx.x == 0) record_error(err, SMOE_ERR_DEVICE);
         }
-        const int n = e < E ? max(1, (r1 - r0 + kRouterItemRows - 1) / kRouterItemRows) : 0;
-        int32_t v = n;
+        int v = n;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const int32_t u = __shfl_up_sync(0xFFFFFFFFu, v, off);
+            const int u = __shfl_up_sync(0xFFFFFFFFu, v, off);
             if (lane >= off) v += u;
         }
         if (lane == 31) warp_tot[w] = v;
+        if (threadIdx.x == 0) found = make_int4(-1, 0, 0, 0);
         __syncthreads();
-        if (w == 0) {
-            int32_t tv = warp_tot[lane];
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int32_t u = __shfl_up_sync(0xFFFFFFFFu, tv, off);
-                if (lane >= off) tv += u;
+        int first = v - n;
+        for (int q = 0; q < w; ++q) first += warp_tot[q];
+        const int item = blockIdx.x;
+        if (item >= first && item < first + n)
+            for (int e = e0; e < e1; ++e) {
+                const int a = bad ? 0 : offsets[e], b = bad ? 0 : offsets[e + 1];
+                const int m = max(1, (b - a + kRouterItemRows - 1) / kRouterItemRows);
+                if (item < first + m) {
+                    const int r = (item - first) * kRouterItemRows;
+                    found = make_int4(e, a + r, min(kRouterItemRows, b - a - r), m);
+                    break;
+                }
+                first += m;
             }
-            warp_tot[lane] = tv;
-        }
         __syncthreads();
-        const int32_t first = v + (w > 0 ? warp_tot[w - 1] : 0) - n;
-        if (e < E) {
-            first_item[e] = first;
-            for (int i = 0; i < n; ++i)
-                items[first + i] = make_int4(e, r0 + i * kRouterItemRows,
-                                             min(kRouterItemRows, r1 - r0 - i * kRouterItemRows), n);
-            if (e == E - 1) first_item[E] = first + n;
+    }
+    const int4 it = found;
+    if (it.x < 0) return;
+    for (int i = threadIdx.x; i < it.z; i += kRbThreads) {
+        const int r = it.y + i;
+        int t = row_token[r];
+        float v = 0.f;
+        bool ok = t >= 0 && t < T;
+        if (ok) {
+            int j = -1;
+            for (int q = 0; q < k; ++q)
+                if (perm_row[(int64_t)t * k + q] == r) j = q;
+            ok = j >= 0;
+            if (ok) v = dlogit(topk_w, dtopk_w, t, j, k, logits[(int64_t)t * E + it.x], inv_c);
         }
-        return;
-    }
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= nrouted) return;
-    const int64_t t = i / k;
-    const int32_t e = topk_idx[i];
-    float g = 0.f;
-    if (e >= 0 && e < E) {
-        const float dwj = dtopk_w[i];
-        float sum = 0.f;
-        for (int q = 0; q < k; ++q) sum = fmaf(topk_w[t * k + q] * inv_c, dwj - dtopk_w[t * k + q], sum);
-        const float rest = 1.0f / (1.0f + expf(logits[t * E + e]));   // 1 - sigmoid(l)
-        g = topk_w[i] * rest * sum;
-    } else {
-        record_error(err, SMOE_ERR_DEVICE);
-    }
-    dlogits[i] = g;
-    const int32_t r = perm_row[i];
-    if (r >= 0 && r < nrouted)
-        dl_row[r] = g;
-    else
-        record_error(err, SMOE_ERR_DEVICE);
-}
-
-constexpr int kWgThreadsRouter = 128;   // 8 features a thread: 1024 features a CTA
-
-// CTA (item, 1024-feature slice): the item's rows in order, fp32. An expert of one item writes dW_r,
-// others their partial sum.
-__global__ void __launch_bounds__(kWgThreadsRouter) router_wgrad_kernel(const uint16_t* __restrict__ x,
-                                                                        const float* __restrict__ dl_row,
-                                                                        const int32_t* __restrict__ row_token,
-                                                                        const int4* __restrict__ items,
-                                                                        const int32_t* __restrict__ first_item, int T,
-                                                                        int E, int H, float* __restrict__ partial,
-                                                                        float* __restrict__ dw, int32_t* err) {
-    __shared__ int32_t tok[kRouterItemRows];
-    __shared__ float g[kRouterItemRows];
-    pdl_wait();
-    pdl_launch_dependents();
-    const int item = blockIdx.x;
-    if (item >= first_item[E]) return;
-    const int4 it = items[item];
-    for (int i = threadIdx.x; i < it.z; i += kWgThreadsRouter) {
-        int32_t t = row_token[it.y + i];
-        float v = dl_row[it.y + i];
-        if (t < 0 || t >= T) {
+        if (!ok) {   // a row that is not its token's
             record_error(err, SMOE_ERR_DEVICE);
             t = 0;
-            v = 0.f;
         }
         tok[i] = t;
         g[i] = v;
     }
     __syncthreads();
-    const int c = blockIdx.y * kWgThreadsRouter + threadIdx.x;   // 8-feature vector
-    if (c >= H / 8) return;
-    const uint4* x4 = reinterpret_cast<const uint4*>(x) + c;
+    const int c = blockIdx.y * kRbThreads + threadIdx.x;   // 8-feature vector
     const int vec = H / 8;
+    if (c >= vec) return;
+    const uint4* x4 = reinterpret_cast<const uint4*>(x) + c;
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
@@ -317,24 +333,40 @@ __global__ void __launch_bounds__(kWgThreadsRouter) router_wgrad_kernel(const ui
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[i] = fmaf(s, f[i], acc[i]);
     }
-    float4* o = reinterpret_cast<float4*>((it.w == 1 ? dw + (size_t)it.x * H : partial + (size_t)item * H) + 8 * c);
+    float4* o = reinterpret_cast<float4*>((it.w == 1 ? dw_router + (size_t)it.x * H : partial + (size_t)blockIdx.x * H) + 8 * c);
     o[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
     o[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
 }
 
-// Experts of several items: their partial sums added in item order.
+// Experts of several items: their partial sums added in item order. The items before an expert's are
+// counted from the offsets, as above.
 __global__ void __launch_bounds__(256) router_wgrad_join_kernel(const float* __restrict__ partial,
-                                                               const int32_t* __restrict__ first_item, int H,
+                                                               const int32_t* __restrict__ offsets, int64_t nrouted, int H,
                                                                float* __restrict__ dw) {
     pdl_wait();
     pdl_launch_dependents();
-    const int e = blockIdx.x;
-    const int a = first_item[e], b = first_item[e + 1];
-    if (b - a <= 1) return;
+    const int e = blockIdx.x, E = gridDim.x;
+    const int n = (offsets[e + 1] - offsets[e] + kRouterItemRows - 1) / kRouterItemRows;
+    if (n <= 1) return;
+    __shared__ int32_t part[8];
+    int before = 0;
+    bool bad = false;
+    for (int q = threadIdx.x; q < E; q += 256) {
+        const int a = offsets[q], b = offsets[q + 1];
+        bad |= a < 0 || b < a || b > nrouted;
+        if (q < e) before += max(1, (b - a + kRouterItemRows - 1) / kRouterItemRows);
+    }
+    if (__syncthreads_or(bad)) return;   // every expert had one empty item
+    before = __reduce_add_sync(0xFFFFFFFFu, before);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = before;
+    __syncthreads();
+    before = 0;
+    for (int q = 0; q < 8; ++q) before += part[q];
     const int c = blockIdx.y * 256 + threadIdx.x;   // 4-feature vector
     if (c >= H / 4) return;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = a; i < b; ++i) {
+#pragma unroll 8
+    for (int i = before; i < before + n; ++i) {
         const float4 v = reinterpret_cast<const float4*>(partial + (size_t)i * H)[c];
         s.x += v.x;
         s.y += v.y;
@@ -385,9 +417,6 @@ BwdLayout bwd_layout(const smoe_config_t& c, int64_t T) {
     L.h = o;    o += align_up((size_t)rows * c.inter * 2);
     L.total = o;
     o = kAlign;
-    L.dl_row = o;   o += align_up((size_t)routed * 4);
-    L.items = o;    o += align_up((size_t)items * sizeof(int4));
-    L.n_items = o;  o += align_up((size_t)(c.n_experts + 1) * 4);
     L.partial = o;  o += align_up((size_t)items * c.hidden * 4);
     if (o > L.total) L.total = o;
     return L;
@@ -422,28 +451,23 @@ cudaError_t launch_permute_backward(const smoe_config_t& c, const uint16_t* dx_r
 cudaError_t launch_route_backward(const smoe_config_t& c, const RouteBackward& b, int64_t T, int32_t* err,
                                   cudaStream_t s) {
     const int E = c.n_experts, H = c.hidden, k = c.top_k;
-    const unsigned blocks = (unsigned)((T * k + 1023) / 1024);
+    const unsigned items = (unsigned)router_max_items(T, k, E), entries = (unsigned)((T * k + kRbThreads - 1) / kRbThreads);
     cudaError_t e;
     {
-        LaunchTimer lt(K_ROUTER_DLOGITS, s);
-        e = launch_pdl(router_dlogits_kernel, dim3(blocks + 1), dim3(1024), 0, s, b.logits, b.topk_idx, b.topk_w,
-                       b.dtopk_w, b.offsets, b.perm_row, (int)T, k, E, 1.0f / c.route_scale, b.dlogits, b.dl_row, b.items,
-                       b.n_items, err);
+        LaunchTimer lt(K_ROUTER_BACKWARD, s);
+        e = launch_pdl(router_backward_kernel, dim3(items + entries, (H + 1023) / 1024), dim3(kRbThreads), 0, s, b.x,
+                       b.logits, b.topk_idx, b.topk_w, b.dtopk_w, b.offsets, b.perm_row, b.row_token, (int)T, k, E, H,
+                       1.0f / c.route_scale, (int)items, b.dlogits, b.partial, b.dw_router, err);
     }
     if (e != cudaSuccess) return e;
-    {
-        LaunchTimer lt(K_ROUTER_WGRAD, s);
-        e = launch_pdl(router_wgrad_kernel, dim3((unsigned)router_max_items(T, k, E), (H + 1023) / 1024),
-                       dim3(kWgThreadsRouter), 0, s, b.x, (const float*)b.dl_row, b.row_token, (const int4*)b.items,
-                       (const int32_t*)b.n_items, (int)T, E, H, b.partial, b.dw_router, err);
-    }
-    if (e != cudaSuccess) return e;
+    launches_add(1);
+    if (T <= kRouterItemRows) return cudaSuccess;   // a token picks an expert once: no expert has a second item
     {
         LaunchTimer lt(K_ROUTER_WGRAD_JOIN, s);
         e = launch_pdl(router_wgrad_join_kernel, dim3(E, (H / 4 + 255) / 256), dim3(256), 0, s, (const float*)b.partial,
-                       (const int32_t*)b.n_items, H, b.dw_router);
+                       b.offsets, T * k, H, b.dw_router);
     }
-    if (e == cudaSuccess) launches_add(3);
+    if (e == cudaSuccess) launches_add(1);
     return e;
 }
 

@@ -83,8 +83,8 @@ enum KernelId {
     K_ROUTER_LOGITS = 0, K_ROUTER_TOPK, K_PERMUTE_HIST, K_PERMUTE_SCAN, K_PERMUTE_SCATTER, K_GATHER_ROWS,
     K_EXPERT_GATEUP, K_EXPERT_DOWN, K_COMBINE, K_PACK_GATEUP, K_PACK_DOWN, K_ROUTER_SPLIT, K_ROUTER_GEMM,
     K_DIAG, K_QUANT_X, K_QUANT_H, K_PACK_FP8, K_EXPERT_GATEUP_SAVE, K_EXPERT_DH, K_EXPERT_DX, K_EXPERT_WGRAD_DOWN,
-    K_EXPERT_WGRAD_GATEUP, K_CHECKPOINT_VALUES, K_COMBINE_BACKWARD, K_PERMUTE_BACKWARD, K_ROUTER_DLOGITS,
-    K_ROUTER_WGRAD, K_ROUTER_WGRAD_JOIN, K_NUM_KERNELS
+    K_EXPERT_WGRAD_GATEUP, K_CHECKPOINT_VALUES, K_COMBINE_BACKWARD, K_PERMUTE_BACKWARD, K_ROUTER_BACKWARD,
+    K_ROUTER_WGRAD_JOIN, K_NUM_KERNELS
 };
 const char* kernel_name(int id);
 
@@ -176,13 +176,13 @@ cudaError_t launch_expert_ffn_backward(const smoe_config_t& c, const ExpertBackw
 struct BwdLayout {
     size_t err = 0;
     size_t dgu = 0, h = 0;                                 // smoe_expert_ffn_backward
-    size_t dl_row = 0, items = 0, n_items = 0, partial = 0;   // smoe_route_backward
+    size_t partial = 0;                                    // smoe_route_backward
     size_t total = 0;
 };
 BwdLayout bwd_layout(const smoe_config_t& c, int64_t T);
 
 // Router weight gradient: rows of an expert are summed in items of at most this many.
-constexpr int kRouterItemRows = 256;
+constexpr int kRouterItemRows = 64;
 inline int64_t router_max_items(int64_t T, int k, int E) { return T * k / kRouterItemRows + E; }
 
 cudaError_t launch_combine_backward(const smoe_config_t& c, const uint16_t* dout, const uint16_t* y,
@@ -198,9 +198,6 @@ struct RouteBackward {
     const float *topk_w, *dtopk_w;
     const int32_t *offsets, *perm_row, *row_token;
     float *dlogits, *dw_router;
-    float* dl_row;       // workspace [T*k]
-    int4* items;         // workspace [router_max_items]: expert, first row, rows, index within the expert
-    int32_t* n_items;    // workspace [E + 1]: first item of each expert, then their number
     float* partial;      // workspace [router_max_items][H]
 };
 cudaError_t launch_route_backward(const smoe_config_t& c, const RouteBackward& b, int64_t T, int32_t* err,
