@@ -212,15 +212,17 @@ __device__ __forceinline__ float dlogit(const float* __restrict__ w, const float
     return w[t * k + j] * (1.0f / (1.0f + expf(l))) * sum;   // 1 / (1 + e^l) = 1 - sigmoid(l)
 }
 
-constexpr int kRbThreads = 128;   // 8 features a thread: 1024 features a CTA
+constexpr int kRbThreads = 256;   // 8 features a thread: 2048 features a CTA
+constexpr int kRbFlight = 8;      // rows in flight a thread
 
 // One launch for both gradients. Item = up to kRouterItemRows rows of one expert (an expert without rows
 // has one empty item, which writes its zeros). CTA (x, y): for x below the item bound, item x's sum over
-// its rows in order, for the 1024 features of slice y; it works out its item from the offsets and its
+// its rows in order, for the 2048 features of slice y; it works out its item from the offsets and its
 // rows' dl from the tokens' weights itself, so nothing has to run before it. Above the bound (y = 0):
-// dlogits of 128 entries each. An expert of one item writes dW_r, the others' items partial sums. Rows
-// are gathered from x in L2 (each is read by k experts), 8 in flight a thread; more and smaller items
-// (64 rows) instead of 256 halved the time of a skewed batch, whose long sums otherwise run alone.
+// dlogits of 256 entries each. An expert of one item writes dW_r, the others' items partial sums. Rows
+// are gathered from x in L2 (each is read by k experts), which bounds it: 4096 skewed tokens read 268 MB in
+// 32 us, 8.4 TB/s; 4 or 16 rows in flight and CTAs of 128 or 512 threads measure within 5% of that.
+// Items of 256 rows instead of 64 took 45 us: the long sums of the popular experts run alone at the end.
 __global__ void __launch_bounds__(kRbThreads) router_backward_kernel(
     const uint16_t* __restrict__ x, const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
     const float* __restrict__ topk_w, const float* __restrict__ dtopk_w, const int32_t* __restrict__ offsets,
@@ -313,12 +315,12 @@ __global__ void __launch_bounds__(kRbThreads) router_backward_kernel(
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
     int r = 0;
-    for (; r + 8 <= it.z; r += 8) {
-        uint4 v[8];
+    for (; r + kRbFlight <= it.z; r += kRbFlight) {
+        uint4 v[kRbFlight];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = x4[(size_t)tok[r + q] * vec];
+        for (int q = 0; q < kRbFlight; ++q) v[q] = x4[(size_t)tok[r + q] * vec];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
+        for (int q = 0; q < kRbFlight; ++q) {
             float f[8];
             unpack8(v[q], f);
             const float s = g[r + q];
@@ -338,7 +340,7 @@ __global__ void __launch_bounds__(kRbThreads) router_backward_kernel(
     o[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
 }
 
-// Experts of several items: their partial sums added in item order. The items before an expert's are
+// Experts of several items: their partial sums added in a fixed order. The items before an expert's are
 // counted from the offsets, as above.
 __global__ void __launch_bounds__(256) router_wgrad_join_kernel(const float* __restrict__ partial,
                                                                const int32_t* __restrict__ offsets, int64_t nrouted, int H,
@@ -362,17 +364,28 @@ __global__ void __launch_bounds__(256) router_wgrad_join_kernel(const float* __r
     __syncthreads();
     before = 0;
     for (int q = 0; q < 8; ++q) before += part[q];
-    const int c = blockIdx.y * 256 + threadIdx.x;   // 4-feature vector
-    if (c >= H / 4) return;
+    // two groups of threads take half of the items each
+    __shared__ float4 half[128];
+    const int col = threadIdx.x & 127, grp = threadIdx.x >> 7, per = (n + 1) / 2;
+    const int c = blockIdx.y * 128 + col;   // 4-feature vector
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < H / 4) {
 #pragma unroll 8
-    for (int i = before; i < before + n; ++i) {
-        const float4 v = reinterpret_cast<const float4*>(partial + (size_t)i * H)[c];
-        s.x += v.x;
-        s.y += v.y;
-        s.z += v.z;
-        s.w += v.w;
+        for (int i = before + grp * per; i < before + min(n, (grp + 1) * per); ++i) {
+            const float4 v = reinterpret_cast<const float4*>(partial + (size_t)i * H)[c];
+            s.x += v.x;
+            s.y += v.y;
+            s.z += v.z;
+            s.w += v.w;
+        }
     }
+    if (grp == 1) half[col] = s;
+    __syncthreads();
+    if (grp != 0 || c >= H / 4) return;
+    s.x += half[col].x;
+    s.y += half[col].y;
+    s.z += half[col].z;
+    s.w += half[col].w;
     reinterpret_cast<float4*>(dw + (size_t)e * H)[c] = s;
 }
 
@@ -386,12 +399,21 @@ __global__ void __launch_bounds__(256) checkpoint_values_kernel(const uint8_t* _
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = (blockIdx.y * 32 + lane) * 16;
     if (col >= cols) return;
+    const int64_t r0 = (int64_t)blockIdx.x * 32 + warp * 4;
+    uint4 q[4];
+    uint32_t e[4];
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int64_t r = (int64_t)blockIdx.x * 32 + warp * 4 + i;
-        if (r >= rows) return;
-        const uint4 q = *reinterpret_cast<const uint4*>(codes + (size_t)r * cols + col);
-        const float s = __uint_as_float((uint32_t)scales[(size_t)(col / 32) * rows + r] << 23);
-        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+        if (r0 + i < rows) {
+            q[i] = *reinterpret_cast<const uint4*>(codes + (size_t)(r0 + i) * cols + col);
+            e[i] = scales[(size_t)(col / 32) * rows + r0 + i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (r0 + i >= rows) return;
+        const float s = __uint_as_float(e[i] << 23);
+        const uint32_t u[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
         uint32_t o[8];
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
@@ -399,7 +421,7 @@ __global__ void __launch_bounds__(256) checkpoint_values_kernel(const uint8_t* _
             o[2 * z] = pack_bf16x2(a.x * s, a.y * s);
             o[2 * z + 1] = pack_bf16x2(b.x * s, b.y * s);
         }
-        uint4* d = reinterpret_cast<uint4*>(gu + (size_t)r * cols + col);
+        uint4* d = reinterpret_cast<uint4*>(gu + (size_t)(r0 + i) * cols + col);
         d[0] = make_uint4(o[0], o[1], o[2], o[3]);
         d[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
@@ -455,7 +477,7 @@ cudaError_t launch_route_backward(const smoe_config_t& c, const RouteBackward& b
     cudaError_t e;
     {
         LaunchTimer lt(K_ROUTER_BACKWARD, s);
-        e = launch_pdl(router_backward_kernel, dim3(items + entries, (H + 1023) / 1024), dim3(kRbThreads), 0, s, b.x,
+        e = launch_pdl(router_backward_kernel, dim3(items + entries, (H / 8 + kRbThreads - 1) / kRbThreads), dim3(kRbThreads), 0, s, b.x,
                        b.logits, b.topk_idx, b.topk_w, b.dtopk_w, b.offsets, b.perm_row, b.row_token, (int)T, k, E, H,
                        1.0f / c.route_scale, (int)items, b.dlogits, b.partial, b.dw_router, err);
     }
@@ -464,7 +486,7 @@ cudaError_t launch_route_backward(const smoe_config_t& c, const RouteBackward& b
     if (T <= kRouterItemRows) return cudaSuccess;   // a token picks an expert once: no expert has a second item
     {
         LaunchTimer lt(K_ROUTER_WGRAD_JOIN, s);
-        e = launch_pdl(router_wgrad_join_kernel, dim3(E, (H / 4 + 255) / 256), dim3(256), 0, s, (const float*)b.partial,
+        e = launch_pdl(router_wgrad_join_kernel, dim3(E, (H / 4 + 127) / 128), dim3(256), 0, s, (const float*)b.partial,
                        b.offsets, T * k, H, b.dw_router);
     }
     if (e == cudaSuccess) launches_add(1);

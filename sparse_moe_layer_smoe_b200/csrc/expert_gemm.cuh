@@ -71,6 +71,13 @@ constexpr int kPairMinTile = SMOE_PAIR_MIN_TILE;
 #ifndef SMOE_PAIR_EPI_WARPS_DOWN
 #define SMOE_PAIR_EPI_WARPS_DOWN 8   // the same for the down GEMM
 #endif
+#ifndef SMOE_PAIR_EPI_WARPS_SAVE
+#define SMOE_PAIR_EPI_WARPS_SAVE 16  // the same for gate/up with the checkpoint: its accumulators of a 256-row tile
+                                     // fill TMEM, so the MMAs wait for the drain (8 warps: 5% slower)
+#endif
+#ifndef SMOE_PAIR_EPI_WARPS_DH
+#define SMOE_PAIR_EPI_WARPS_DH 8     // the same for dh
+#endif
 
 struct GemmMaps {
     CUtensorMap w;                  // weights [rows][K]: box {BK, 256 (gate/up) or 128 (down)}
@@ -136,7 +143,12 @@ constexpr KernelId mode_kernel() {
 
 // CTA-pair kernels: producer warp, MMA warp and the epilogue warps of their mode
 template <int MODE>
-__host__ __device__ constexpr int pair_epi_warps() { return MODE == MODE_DOWN ? SMOE_PAIR_EPI_WARPS_DOWN : SMOE_PAIR_EPI_WARPS; }
+__host__ __device__ constexpr int pair_epi_warps() {
+    return MODE == MODE_DOWN || MODE == MODE_DX ? SMOE_PAIR_EPI_WARPS_DOWN
+           : MODE == MODE_GATEUP_SAVE           ? SMOE_PAIR_EPI_WARPS_SAVE
+           : MODE == MODE_DH                    ? SMOE_PAIR_EPI_WARPS_DH
+                                                : SMOE_PAIR_EPI_WARPS;
+}
 template <int MODE>
 __host__ __device__ constexpr int pair_threads() { return 64 + 32 * pair_epi_warps<MODE>(); }
 

@@ -493,6 +493,26 @@ def test_training_step_against_the_oracle(name):
         norm(_np(o["dws_" + key]), at[E], "shared " + key)
 
 
+def test_layer_training_methods_are_the_chain():
+    name = "tiny"
+    T = SHAPES[name][0]
+    packed, W, x, x64, wr, wr64, dout, dout64, bias, _ = _chain_inputs(name, 44)
+    cfg = _cfg(name)
+    want = _chain(cfg, x, wr, bias, packed, dout, _ws(cfg, T))
+    layer = smoe.MoELayer(cfg, wr, bias, packed)
+    out, saved = layer.forward_train(x)
+    got = dict(layer.backward(saved, dout), out=out)
+    got["dwr"] = got.pop("dw_router")
+    for key, v in got.items():
+        assert torch.equal(v.view(torch.uint8), want[key].view(torch.uint8)), key
+    for t in (0, 1):      # no tokens, and one
+        o, s = layer.forward_train(x[:t].contiguous())
+        g = layer.backward(s, dout[:t].contiguous())
+        assert o.shape == (t, cfg.hidden) and g["dx"].shape == (t, cfg.hidden)
+        assert all(torch.isfinite(v.float()).all() for v in g.values())
+        assert t or not any(g[key].any() for key in g if key.startswith("dw"))
+
+
 @pytest.mark.parametrize("name", ["tiny", "pairs"])
 def test_training_step_captured_and_on_another_stream(name):
     """The chain captured into a graph and replayed twice, and run on a side stream, gives the eager bits."""
