@@ -108,67 +108,30 @@ __global__ void __launch_bounds__(256, 3) combine_backward_kernel(const uint16_t
     }
 }
 
-// One CTA per token. The router's term is left out when dlogits is null. With it a token reads 16 KB of the
-// router's weights for each of its experts (at H = 4096), more than the rows themselves, but from L2: 8192
-// tokens take 129 us, 5.2 TB/s of HBM beside as much again and half from L2. Four CTAs an SM matter (three:
-// 139 us, two: 163). Keeping the weights of a 128-feature slice of all experts in shared memory, so that
-// only the rows cross L2, was slower: 228 us, as rows are then read in 256-byte pieces.
-__global__ void __launch_bounds__(256, 4) permute_backward_kernel(const uint16_t* __restrict__ dx_rows,
-                                                               const int32_t* __restrict__ perm_row,
-                                                               const int32_t* __restrict__ topk_idx,
-                                                               const float* __restrict__ dlogits,
-                                                               const float* __restrict__ w_router, int T, int k, int E,
-                                                               int H, uint16_t* __restrict__ dx, int32_t* err) {
-    __shared__ int32_t rows[32], experts[32];
-    __shared__ float dl[32];
-    pdl_wait();
-    pdl_launch_dependents();
-    const int t = blockIdx.x;
+// One token's dx, by the threads of a CTA. rows, experts, dl: 32 slots each (rows -1: none).
+template <bool ROUTER>
+__device__ __forceinline__ void permute_backward_row(const uint4* __restrict__ rows4, const uint4* __restrict__ own,
+                                                     const float* __restrict__ w_router, const int32_t* rows,
+                                                     const int32_t* experts, const float* dl, int k, int H,
+                                                     uint4* __restrict__ out) {
     const int vec = H / 8;
-    const int64_t nrouted = (int64_t)T * k;
-    if (threadIdx.x < 32) {
-        const size_t i = (size_t)t * k + threadIdx.x;
-        int32_t r = -1, e = 0;
-        float g = 0.f;
-        const bool entry = (int)threadIdx.x < k;
-        if (entry) r = perm_row[i];
-        if (entry && (r < 0 || r >= nrouted)) {
-            record_error(err, SMOE_ERR_DEVICE);
-            r = -1;
-        }
-        if (entry && dlogits != nullptr) {
-            e = topk_idx[i];
-            g = dlogits[i];
-            if (e < 0 || e >= E) {
-                record_error(err, SMOE_ERR_DEVICE);
-                e = 0;
-                g = 0.f;
-            }
-        }
-        rows[threadIdx.x] = r;
-        experts[threadIdx.x] = e;
-        dl[threadIdx.x] = g;
-    }
-    __syncthreads();
-    const bool router = dlogits != nullptr;
     for (int c = threadIdx.x; c < vec; c += blockDim.x) {
         float acc[8];
-        unpack8(reinterpret_cast<const uint4*>(dx_rows)[(size_t)(nrouted + t) * vec + c], acc);
+        unpack8(own[c], acc);
         for (int j0 = 0; j0 < k; j0 += kSlots) {
             // the rows and the first router weights in flight together, then the rest of the weights
             uint4 v[kSlots];
 #pragma unroll
             for (int j = 0; j < kSlots; ++j) {
                 v[j] = make_uint4(0u, 0u, 0u, 0u);
-                if (rows[j0 + j] >= 0) v[j] = reinterpret_cast<const uint4*>(dx_rows)[(size_t)rows[j0 + j] * vec + c];
+                if (rows[j0 + j] >= 0) v[j] = rows4[(size_t)rows[j0 + j] * vec + c];
             }
 #pragma unroll
             for (int z = 0; z < kSlots; z += kAhead) {
                 float4 a[kAhead], b[kAhead];
-                if (router) {
+                if (ROUTER) {
 #pragma unroll
                     for (int j = 0; j < kAhead; ++j) {
-                        // a skipped entry has weight 0 on expert 0's row
                         const float4* w4 = reinterpret_cast<const float4*>(w_router + (size_t)experts[j0 + z + j] * H) + 2 * c;
                         a[j] = w4[0];
                         b[j] = w4[1];
@@ -183,7 +146,7 @@ __global__ void __launch_bounds__(256, 4) permute_backward_kernel(const uint16_t
                         for (int i = 0; i < 8; ++i) acc[i] += f[i];
                     }
                 }
-                if (router) {
+                if (ROUTER) {
 #pragma unroll
                     for (int j = 0; j < kAhead; ++j) {
                         const float g = dl[j0 + z + j];
@@ -199,8 +162,65 @@ __global__ void __launch_bounds__(256, 4) permute_backward_kernel(const uint16_t
                 }
             }
         }
-        reinterpret_cast<uint4*>(dx)[(size_t)t * vec + c] = pack8(acc);
+        out[c] = pack8(acc);
     }
+}
+
+// One CTA per token. The router's term is left out when dlogits is null. With it a token reads 16 KB of the
+// router's weights for each of its experts (at H = 4096), more than the rows themselves, but from L2: 8192
+// tokens take 129 us, 5.2 TB/s of HBM beside as much again and half from L2. Four CTAs an SM matter (three:
+// 139 us, two: 163). Keeping the weights of a 128-feature slice of all experts in shared memory, so that
+// only the rows cross L2, was slower: 228 us, as rows are then read in 256-byte pieces.
+__global__ void __launch_bounds__(256, 4) permute_backward_kernel(const uint16_t* __restrict__ dx_rows,
+                                                               const int32_t* __restrict__ perm_row,
+                                                               const int32_t* __restrict__ topk_idx,
+                                                               const float* __restrict__ dlogits,
+                                                               const float* __restrict__ w_router, int T, int k, int E,
+                                                               int H, uint16_t* __restrict__ dx, int32_t* err) {
+    __shared__ int32_t rows[32], experts[32];
+    __shared__ float dl[32];
+    __shared__ bool any_expert;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int t = blockIdx.x;
+    const int vec = H / 8;
+    const int64_t nrouted = (int64_t)T * k;
+    if (threadIdx.x < 32) {
+        const size_t i = (size_t)t * k + threadIdx.x;
+        int32_t r = -1, e = -1;
+        float g = 0.f;
+        const bool entry = (int)threadIdx.x < k;
+        if (entry) r = perm_row[i];
+        if (entry && (r < 0 || r >= nrouted)) {
+            record_error(err, SMOE_ERR_DEVICE);
+            r = -1;
+        }
+        if (entry && dlogits != nullptr) {
+            e = topk_idx[i];
+            g = dlogits[i];
+            if (e < 0 || e >= E) {
+                record_error(err, SMOE_ERR_DEVICE);
+                e = -1;
+                g = 0.f;
+            }
+        }
+        rows[threadIdx.x] = r;
+        // slots past k and skipped entries repeat one of the token's own experts with weight 0, so that the
+        // loop needs no branch and no other expert's weights are read
+        const unsigned valid = __ballot_sync(0xFFFFFFFFu, e >= 0);
+        const int32_t own = __shfl_sync(0xFFFFFFFFu, e, valid ? __ffs(valid) - 1 : 0);
+        experts[threadIdx.x] = e >= 0 ? e : own;
+        dl[threadIdx.x] = g;
+        if (threadIdx.x == 0) any_expert = valid != 0;
+    }
+    __syncthreads();
+    const uint4* rows4 = reinterpret_cast<const uint4*>(dx_rows);
+    const uint4* own = rows4 + (size_t)(nrouted + t) * vec;
+    uint4* out = reinterpret_cast<uint4*>(dx) + (size_t)t * vec;
+    if (any_expert)   // false without dlogits
+        permute_backward_row<true>(rows4, own, w_router, rows, experts, dl, k, H, out);
+    else
+        permute_backward_row<false>(rows4, own, w_router, rows, experts, dl, k, H, out);
 }
 
 // dl of entry i = t * k + j, whose selected logit is l.
@@ -287,30 +307,32 @@ __global__ void __launch_bounds__(kRbThreads) router_backward_kernel(
     }
     const int4 it = found;
     if (it.x < 0) return;
-    for (int i = threadIdx.x; i < it.z; i += kRbThreads) {
-        const int r = it.y + i;
-        int t = row_token[r];
-        float v = 0.f;
+    static_assert(kRouterItemRows <= kRbThreads, "one row of an item a thread");
+    int my_t = -1;
+    if ((int)threadIdx.x < it.z) {
+        my_t = row_token[it.y + threadIdx.x];
+        tok[threadIdx.x] = my_t >= 0 && my_t < T ? my_t : 0;
+    }
+    __syncthreads();
+    const int c = blockIdx.y * kRbThreads + threadIdx.x;   // 8-feature vector
+    const int vec = H / 8;
+    const uint4* x4 = reinterpret_cast<const uint4*>(x) + c;
+    if ((int)threadIdx.x < it.z) {
+        const int r = it.y + threadIdx.x, t = my_t;
+        float d = 0.f;
         bool ok = t >= 0 && t < T;
         if (ok) {
             int j = -1;
             for (int q = 0; q < k; ++q)
                 if (perm_row[(int64_t)t * k + q] == r) j = q;
             ok = j >= 0;
-            if (ok) v = dlogit(topk_w, dtopk_w, t, j, k, logits[(int64_t)t * E + it.x], inv_c);
+            if (ok) d = dlogit(topk_w, dtopk_w, t, j, k, logits[(int64_t)t * E + it.x], inv_c);
         }
-        if (!ok) {   // a row that is not its token's
-            record_error(err, SMOE_ERR_DEVICE);
-            t = 0;
-        }
-        tok[i] = t;
-        g[i] = v;
+        if (!ok) record_error(err, SMOE_ERR_DEVICE);   // a row that is not its token's
+        g[threadIdx.x] = d;
     }
     __syncthreads();
-    const int c = blockIdx.y * kRbThreads + threadIdx.x;   // 8-feature vector
-    const int vec = H / 8;
     if (c >= vec) return;
-    const uint4* x4 = reinterpret_cast<const uint4*>(x) + c;
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;

@@ -498,8 +498,8 @@ __device__ __forceinline__ void epi_swiglu_backward(const GemmParams& p, uint32_
                 float g = q.x * kg, u = q.y * ku;
                 bool pass_g = true, pass_u = true;
                 if (lim > 0.0f) {
-                    pass_g = !(g > lim);
-                    pass_u = !(fabsf(u) > lim);
+                    pass_g = g <= lim;
+                    pass_u = fabsf(u) <= lim;
                     g = fminf(g, lim);
                     u = fminf(fmaxf(u, -lim), lim);
                 }

@@ -149,6 +149,25 @@ def test_permute_backward(name, router):
     _within(_np(dx), ref, np.abs(ref) * U + (2 * k + 2) * F * (1 + U) * terms, "dx")
 
 
+@pytest.mark.parametrize("k", [1, 3, 5, 20])
+def test_permute_backward_reads_no_other_experts_weights(k):
+    """Experts that a token did not choose may hold anything, expert 0 too."""
+    T, H, E = 20, 128, 24
+    cfg = smoe.config(H, E, k, 128, 128, 3.0)
+    rng = np.random.default_rng(15)
+    idx = np.stack([1 + rng.permutation(E - 2)[:k] for _ in range(T)]).astype(np.int32)   # never 0 or E - 1
+    perm_row = moe.permute(idx, E)[2]
+    wr, wr64 = _f32(rng.normal(size=(E, H)))
+    wr[0], wr[E - 1] = float("inf"), float("nan")
+    dxr, dxr64 = _bf16(rng.normal(size=(T * k + T, H)))
+    dl, dl64 = _f32(rng.normal(size=(T, k)))
+    dx = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    smoe.smoe_permute_backward(cfg, dxr, _i32(perm_row), _i32(idx), dl, wr, T, dx, _ws(cfg, T))
+    ref = ob.permute_backward(dxr64, perm_row, idx, dl64, wr64)
+    terms = ob.permute_backward(np.abs(dxr64), perm_row, idx, np.abs(dl64), np.abs(wr64))
+    _within(_np(dx), ref, np.abs(ref) * U + (2 * k + 2) * F * (1 + U) * terms, "dx")
+
+
 def _route_backward(name, rng, r=None):
     T, H, E, k, I, _, _ = SHAPES[name]
     r, cfg = r or _routing(name, rng), _cfg(name)
