@@ -253,32 +253,44 @@ def smoe_forward_fp8(cfg, x, T, w_router, bias, packed_fp8, out, ws=None, ws_byt
 _dtypes = {}   # name -> torch dtype, filled on the first checked call
 
 
-def _pointers(fn: str, T: int, *args) -> list:
-    """The pointers of (name, tensor, dtype, n) arguments. A torch tensor must hold at least n elements of that
-    type, contiguous, on the current CUDA device (whose current stream the call goes to). Raw pointers and
-    None are passed on as they are: the library checks them."""
+def _pointers_py(fn: str, T: int, *args) -> list:
+    """The pointers of (name, tensor, dtype, n) arguments, given flat. A torch tensor must hold at least n
+    elements of that type, contiguous, on the current CUDA device (whose current stream the call goes to). Raw
+    pointers and None are passed on as they are: the library checks them."""
     if not _dtypes:
         import torch
         _dtypes.update({n: getattr(torch, n) for n in ("bfloat16", "float32", "int32", "uint8")})
     here = _current()[0]() if T > 0 else None
     out = []
-    for name, t, dtype, n in args:
+    for name, t, dtype, n in zip(*(iter(args),) * 4):
         if t is None or type(t) is int:
             out.append(t)
             continue
-        if not (t.dtype is _dtypes[dtype] and t.numel() >= n and t.is_contiguous()
-                and (here is None or t.get_device() == here)):
-            if t.dtype is not _dtypes[dtype]:
-                why = f"{name} is {t.dtype}, not torch.{dtype}"
-            elif not t.is_contiguous():
-                why = f"{name} is not contiguous"
-            elif t.numel() < n:
-                why = f"{name} has {t.numel()} elements, {n} are needed"
-            else:
-                why = f"{name} is on {t.device}, the call runs on cuda:{here}"
+        why = None
+        if t.dtype is not _dtypes[dtype]:
+            why = f"{name} is {t.dtype}, not torch.{dtype}"
+        elif not t.is_contiguous():
+            why = f"{name} is not contiguous"
+        elif t.numel() < n:
+            why = f"{name} has {t.numel()} elements, {n} are needed"
+        elif here is not None and t.get_device() != here:
+            why = f"{name} is on {t.device}, the call runs on cuda:{here}"
+        if why:
             raise SmoeError(fn, SMOE_ERR_INVALID_ARG, why)
         out.append(t.data_ptr())
     return out
+
+
+_pointers_native = None   # the same check in the _pyargs module
+
+
+def _pointers(fn: str, T: int, *args) -> list:
+    global _pointers, _pointers_native
+    import torch  # noqa: F401  (the module links against its libraries)
+    from . import _pyargs
+    _pyargs.use(_pointers_py)
+    _pointers = _pointers_native = _pyargs.pointers   # from the second call on, without this function
+    return _pointers(fn, T, *args)
 
 
 def smoe_backward_bytes(cfg: SmoeConfig, T: int) -> int:
@@ -289,10 +301,10 @@ def smoe_expert_ffn_save(cfg, x, x_perm, row_token, offsets, T, packed, y, gu_q,
                          stream=None):
     """smoe_expert_ffn with the 8-bit checkpoint of the gate and up products (see include/stepmoe.h)."""
     H, I, R = cfg.hidden, cfg.inter, T * cfg.top_k
-    p = _pointers("smoe_expert_ffn_save", T, ("x", x, "bfloat16", T * H), ("x_perm", x_perm, "bfloat16", R * H),
-                  ("row_token", row_token, "int32", R), ("offsets", offsets, "int32", cfg.n_experts + 1),
-                  ("y", y, "bfloat16", (R + T) * H), ("gu_q", gu_q, "uint8", (R + T) * 2 * I),
-                  ("gu_scale", gu_scale, "uint8", 2 * I // 32 * (R + T)))
+    p = _pointers("smoe_expert_ffn_save", T, "x", x, "bfloat16", T * H, "x_perm", x_perm, "bfloat16", R * H,
+                  "row_token", row_token, "int32", R, "offsets", offsets, "int32", cfg.n_experts + 1,
+                  "y", y, "bfloat16", (R + T) * H, "gu_q", gu_q, "uint8", (R + T) * 2 * I,
+                  "gu_scale", gu_scale, "uint8", 2 * I // 32 * (R + T))
     _check("smoe_expert_ffn_save", lib().smoe_expert_ffn_save(ctypes.byref(cfg), *p[:4], T, _p(packed), *p[4:], _p(ws),
                                                               _ws_bytes(ws, ws_bytes), _s(stream)))
 
@@ -300,16 +312,16 @@ def smoe_expert_ffn_save(cfg, x, x_perm, row_token, offsets, T, packed, y, gu_q,
 def smoe_checkpoint_values(cfg, gu_q, gu_scale, T, gu, stream=None):
     """The bf16 values a checkpoint stands for."""
     I, rows = cfg.inter, T * cfg.top_k + T
-    p = _pointers("smoe_checkpoint_values", T, ("gu_q", gu_q, "uint8", rows * 2 * I),
-                  ("gu_scale", gu_scale, "uint8", 2 * I // 32 * rows), ("gu", gu, "bfloat16", rows * 2 * I))
+    p = _pointers("smoe_checkpoint_values", T, "gu_q", gu_q, "uint8", rows * 2 * I,
+                  "gu_scale", gu_scale, "uint8", 2 * I // 32 * rows, "gu", gu, "bfloat16", rows * 2 * I)
     _check("smoe_checkpoint_values", lib().smoe_checkpoint_values(ctypes.byref(cfg), p[0], p[1], T, p[2], _s(stream)))
 
 
 def smoe_combine_backward(cfg, dout, y, perm_row, topk_w, T, dy, dtopk_w, ws=None, ws_bytes=None, stream=None):
     H, R = cfg.hidden, T * cfg.top_k
-    p = _pointers("smoe_combine_backward", T, ("dout", dout, "bfloat16", T * H), ("y", y, "bfloat16", (R + T) * H),
-                  ("perm_row", perm_row, "int32", R), ("topk_w", topk_w, "float32", R), ("dy", dy, "bfloat16", R * H),
-                  ("dtopk_w", dtopk_w, "float32", R))
+    p = _pointers("smoe_combine_backward", T, "dout", dout, "bfloat16", T * H, "y", y, "bfloat16", (R + T) * H,
+                  "perm_row", perm_row, "int32", R, "topk_w", topk_w, "float32", R, "dy", dy, "bfloat16", R * H,
+                  "dtopk_w", dtopk_w, "float32", R)
     _check("smoe_combine_backward", lib().smoe_combine_backward(ctypes.byref(cfg), *p[:4], T, *p[4:], _p(ws),
                                                                 _ws_bytes(ws, ws_bytes), _s(stream)))
 
@@ -317,11 +329,11 @@ def smoe_combine_backward(cfg, dout, y, perm_row, topk_w, T, dy, dtopk_w, ws=Non
 def smoe_route_backward(cfg, x, T, logits, topk_idx, topk_w, dtopk_w, offsets, perm_row, row_token, dlogits, dw_router,
                         ws=None, ws_bytes=None, stream=None):
     H, E, R = cfg.hidden, cfg.n_experts, T * cfg.top_k
-    p = _pointers("smoe_route_backward", T, ("x", x, "bfloat16", T * H), ("logits", logits, "float32", T * E),
-                  ("topk_idx", topk_idx, "int32", R), ("topk_w", topk_w, "float32", R),
-                  ("dtopk_w", dtopk_w, "float32", R), ("offsets", offsets, "int32", E + 1),
-                  ("perm_row", perm_row, "int32", R), ("row_token", row_token, "int32", R),
-                  ("dlogits", dlogits, "float32", R), ("dw_router", dw_router, "float32", E * H))
+    p = _pointers("smoe_route_backward", T, "x", x, "bfloat16", T * H, "logits", logits, "float32", T * E,
+                  "topk_idx", topk_idx, "int32", R, "topk_w", topk_w, "float32", R,
+                  "dtopk_w", dtopk_w, "float32", R, "offsets", offsets, "int32", E + 1,
+                  "perm_row", perm_row, "int32", R, "row_token", row_token, "int32", R,
+                  "dlogits", dlogits, "float32", R, "dw_router", dw_router, "float32", E * H)
     _check("smoe_route_backward", lib().smoe_route_backward(ctypes.byref(cfg), p[0], T, *p[1:], _p(ws),
                                                             _ws_bytes(ws, ws_bytes), _s(stream)))
 
@@ -330,13 +342,13 @@ def smoe_expert_ffn_backward(cfg, x, x_perm, offsets, T, packed, gu_q, gu_scale,
                              dw_down, dws_gate, dws_up, dws_down, ws=None, ws_bytes=None, stream=None):
     H, E, I, R = cfg.hidden, cfg.n_experts, cfg.inter, T * cfg.top_k
     w = H * I
-    p = _pointers("smoe_expert_ffn_backward", T, ("x", x, "bfloat16", T * H), ("x_perm", x_perm, "bfloat16", R * H),
-                  ("offsets", offsets, "int32", E + 1), ("gu_q", gu_q, "uint8", (R + T) * 2 * I),
-                  ("gu_scale", gu_scale, "uint8", 2 * I // 32 * (R + T)), ("dy", dy, "bfloat16", R * H),
-                  ("dout", dout, "bfloat16", T * H), ("dx_rows", dx_rows, "bfloat16", (R + T) * H),
-                  ("dw_gate", dw_gate, "bfloat16", E * w), ("dw_up", dw_up, "bfloat16", E * w),
-                  ("dw_down", dw_down, "bfloat16", E * w), ("dws_gate", dws_gate, "bfloat16", w),
-                  ("dws_up", dws_up, "bfloat16", w), ("dws_down", dws_down, "bfloat16", w))
+    p = _pointers("smoe_expert_ffn_backward", T, "x", x, "bfloat16", T * H, "x_perm", x_perm, "bfloat16", R * H,
+                  "offsets", offsets, "int32", E + 1, "gu_q", gu_q, "uint8", (R + T) * 2 * I,
+                  "gu_scale", gu_scale, "uint8", 2 * I // 32 * (R + T), "dy", dy, "bfloat16", R * H,
+                  "dout", dout, "bfloat16", T * H, "dx_rows", dx_rows, "bfloat16", (R + T) * H,
+                  "dw_gate", dw_gate, "bfloat16", E * w, "dw_up", dw_up, "bfloat16", E * w,
+                  "dw_down", dw_down, "bfloat16", E * w, "dws_gate", dws_gate, "bfloat16", w,
+                  "dws_up", dws_up, "bfloat16", w, "dws_down", dws_down, "bfloat16", w)
     _check("smoe_expert_ffn_backward", lib().smoe_expert_ffn_backward(ctypes.byref(cfg), *p[:3], T, _p(packed), *p[3:],
                                                                       _p(ws), _ws_bytes(ws, ws_bytes), _s(stream)))
 
@@ -344,9 +356,9 @@ def smoe_expert_ffn_backward(cfg, x, x_perm, offsets, T, packed, gu_q, gu_scale,
 def smoe_permute_backward(cfg, dx_rows, perm_row, topk_idx, dlogits, w_router, T, dx, ws=None, ws_bytes=None,
                           stream=None):
     H, E, R = cfg.hidden, cfg.n_experts, T * cfg.top_k
-    p = _pointers("smoe_permute_backward", T, ("dx_rows", dx_rows, "bfloat16", (R + T) * H),
-                  ("perm_row", perm_row, "int32", R), ("topk_idx", topk_idx, "int32", R),
-                  ("dlogits", dlogits, "float32", R), ("w_router", w_router, "float32", E * H), ("dx", dx, "bfloat16", T * H))
+    p = _pointers("smoe_permute_backward", T, "dx_rows", dx_rows, "bfloat16", (R + T) * H,
+                  "perm_row", perm_row, "int32", R, "topk_idx", topk_idx, "int32", R,
+                  "dlogits", dlogits, "float32", R, "w_router", w_router, "float32", E * H, "dx", dx, "bfloat16", T * H)
     _check("smoe_permute_backward", lib().smoe_permute_backward(ctypes.byref(cfg), *p[:5], T, p[5], _p(ws),
                                                                 _ws_bytes(ws, ws_bytes), _s(stream)))
 
