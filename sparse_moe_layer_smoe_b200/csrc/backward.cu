@@ -240,9 +240,10 @@ constexpr int kRbFlight = 8;      // rows in flight a thread
 // its rows in order, for the 2048 features of slice y; it works out its item from the offsets and its
 // rows' dl from the tokens' weights itself, so nothing has to run before it. Above the bound (y = 0):
 // dlogits of 256 entries each. An expert of one item writes dW_r, the others' items partial sums. Rows
-// are gathered from x in L2 (each is read by k experts), which bounds it: 4096 skewed tokens read 268 MB in
-// 32 us, 8.4 TB/s; 4 or 16 rows in flight and CTAs of 128 or 512 threads measure within 5% of that.
-// Items of 256 rows instead of 64 took 45 us: the long sums of the popular experts run alone at the end.
+// are gathered from x in L2 (each is read by k experts), which bounds it: 4096 tokens read 268 MB in 31 us,
+// 8.6 TB/s; 4 or 16 rows in flight and CTAs of 128 or 512 threads measure within 5% of that. Items of 256
+// rows instead of 64: the same on even batches, but 46 us instead of 35 on a skewed one of 4096 tokens and
+// 29 instead of 14 on one of 257, whose popular experts' long sums run alone at the end.
 __global__ void __launch_bounds__(kRbThreads) router_backward_kernel(
     const uint16_t* __restrict__ x, const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
     const float* __restrict__ topk_w, const float* __restrict__ dtopk_w, const int32_t* __restrict__ offsets,
@@ -411,23 +412,24 @@ __global__ void __launch_bounds__(256) router_wgrad_join_kernel(const float* __r
     reinterpret_cast<float4*>(dw + (size_t)e * H)[c] = s;
 }
 
-// Values of the checkpoint: bf16 holds a code times its scale exactly (short of bf16's own range). Block:
-// 32 rows, so that a 32-byte sector of the column-wise scales serves all of them; a lane takes 16 codes.
+// Values of the checkpoint: bf16 holds a code times its scale exactly (short of bf16's own range). A lane
+// takes 8 codes, so that a warp's stores are contiguous (16 codes and two stores: 150 us instead of 109 for
+// 8192 tokens, 0.57 GB); a block 32 rows, so that a 32-byte sector of the column-wise scales serves all.
 __global__ void __launch_bounds__(256) checkpoint_values_kernel(const uint8_t* __restrict__ codes,
                                                                const uint8_t* __restrict__ scales, int64_t rows, int cols,
                                                                uint16_t* __restrict__ gu) {
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int col = (blockIdx.y * 32 + lane) * 16;
+    const int col = (blockIdx.y * 32 + lane) * 8;
     if (col >= cols) return;
     const int64_t r0 = (int64_t)blockIdx.x * 32 + warp * 4;
-    uint4 q[4];
+    uint2 q[4];
     uint32_t e[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if (r0 + i < rows) {
-            q[i] = *reinterpret_cast<const uint4*>(codes + (size_t)(r0 + i) * cols + col);
+            q[i] = *reinterpret_cast<const uint2*>(codes + (size_t)(r0 + i) * cols + col);
             e[i] = scales[(size_t)(col / 32) * rows + r0 + i];
         }
     }
@@ -435,17 +437,11 @@ __global__ void __launch_bounds__(256) checkpoint_values_kernel(const uint8_t* _
     for (int i = 0; i < 4; ++i) {
         if (r0 + i >= rows) return;
         const float s = __uint_as_float(e[i] << 23);
-        const uint32_t u[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-        uint32_t o[8];
-#pragma unroll
-        for (int z = 0; z < 4; ++z) {
-            const float2 a = e4m3x2_to_float2(u[z] & 0xFFFFu), b = e4m3x2_to_float2(u[z] >> 16);
-            o[2 * z] = pack_bf16x2(a.x * s, a.y * s);
-            o[2 * z + 1] = pack_bf16x2(b.x * s, b.y * s);
-        }
-        uint4* d = reinterpret_cast<uint4*>(gu + (size_t)(r0 + i) * cols + col);
-        d[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        const float2 a = e4m3x2_to_float2(q[i].x & 0xFFFFu), b = e4m3x2_to_float2(q[i].x >> 16);
+        const float2 c = e4m3x2_to_float2(q[i].y & 0xFFFFu), d = e4m3x2_to_float2(q[i].y >> 16);
+        *reinterpret_cast<uint4*>(gu + (size_t)(r0 + i) * cols + col) =
+            make_uint4(pack_bf16x2(a.x * s, a.y * s), pack_bf16x2(b.x * s, b.y * s), pack_bf16x2(c.x * s, c.y * s),
+                       pack_bf16x2(d.x * s, d.y * s));
     }
 }
 
@@ -521,7 +517,7 @@ cudaError_t launch_checkpoint_values(const smoe_config_t& c, const uint8_t* code
     cudaError_t e;
     {
         LaunchTimer lt(K_CHECKPOINT_VALUES, s);
-        e = launch_pdl(checkpoint_values_kernel, dim3((unsigned)((rows + 31) / 32), (cols + 511) / 512), dim3(256), 0, s,
+        e = launch_pdl(checkpoint_values_kernel, dim3((unsigned)((rows + 31) / 32), (cols + 255) / 256), dim3(256), 0, s,
                        codes, scales, rows, cols, gu);
     }
     if (e == cudaSuccess) launches_add(1);
