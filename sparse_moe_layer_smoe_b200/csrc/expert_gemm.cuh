@@ -408,7 +408,8 @@ __device__ __forceinline__ uint32_t ck_scale_byte(uint32_t absmax_bits) {
 
 // Columns of a unit that a training epilogue takes at a time. Its loop over them is not unrolled: with
 // every column of a unit unrolled (as epi_load is, for far fewer instructions a column) the code
-// outgrows the instruction cache, and the warps spend most of their time waiting for instructions.
+// outgrows the instruction cache, and the warps spend most of their time waiting for instructions (8192
+// tokens: dh 1717 us unrolled, 1068 us looped; gate/up with the checkpoint 2338 and 1731 us).
 constexpr int kTrainCols = 16;
 
 // Saving gate/up: drains the accumulators like epi_load and epi_store, and writes the checkpoint of the
