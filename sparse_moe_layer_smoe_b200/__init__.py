@@ -253,21 +253,22 @@ def smoe_forward_fp8(cfg, x, T, w_router, bias, packed_fp8, out, ws=None, ws_byt
 _dtypes = {}   # name -> torch dtype, filled on the first checked call
 
 
-def _pointers_py(fn: str, T: int, *args) -> list:
-    """The pointers of (name, tensor, dtype, n) arguments, given flat. A torch tensor must hold at least n
-    elements of that type, contiguous, on the current CUDA device (whose current stream the call goes to). Raw
-    pointers and None are passed on as they are: the library checks them."""
+def _arguments_py(fn: str, T: int, ws, ws_bytes, stream, *args) -> list:
+    """The pointers of (name, tensor, dtype, n) arguments, given flat, then the workspace's pointer and bytes and the
+    stream. A torch tensor must hold at least n elements of that type, contiguous, on the current CUDA device
+    (whose current stream the call goes to); the workspace too must be there. Raw pointers and None are passed on
+    as they are: the library checks them."""
     if not _dtypes:
         import torch
         _dtypes.update({n: getattr(torch, n) for n in ("bfloat16", "float32", "int32", "uint8")})
     here = _current()[0]() if T > 0 else None
     out = []
-    for name, t, dtype, n in zip(*(iter(args),) * 4):
+    for name, t, dtype, n in zip(*(iter((*args, "ws", ws, None, 0)),) * 4):
         if t is None or type(t) is int:
             out.append(t)
             continue
         why = None
-        if t.dtype is not _dtypes[dtype]:
+        if dtype is not None and t.dtype is not _dtypes[dtype]:
             why = f"{name} is {t.dtype}, not torch.{dtype}"
         elif not t.is_contiguous():
             why = f"{name} is not contiguous"
@@ -278,19 +279,23 @@ def _pointers_py(fn: str, T: int, *args) -> list:
         if why:
             raise SmoeError(fn, SMOE_ERR_INVALID_ARG, why)
         out.append(t.data_ptr())
-    return out
+    return [*out, _ws_bytes(ws, ws_bytes), _s(stream) if T > 0 or stream is not None else _stream_or_default()]
 
 
-_pointers_native = None   # the same check in the _pyargs module
+def _stream_or_default():
+    """The current stream, or the default one where there is no CUDA device (calls with T == 0)."""
+    import torch
+    return _s(None) if torch.cuda.is_available() else None
 
 
-def _pointers(fn: str, T: int, *args) -> list:
-    global _pointers, _pointers_native
+def _arguments(fn: str, T: int, *args) -> list:
+    """_arguments_py, from the first call on through the native module."""
+    global _arguments
     import torch  # noqa: F401  (the module links against its libraries)
     from . import _pyargs
-    _pyargs.use(_pointers_py)
-    _pointers = _pointers_native = _pyargs.pointers   # from the second call on, without this function
-    return _pointers(fn, T, *args)
+    _pyargs.use(_arguments_py)
+    _arguments = _pyargs.arguments
+    return _arguments(fn, T, *args)
 
 
 def smoe_backward_bytes(cfg: SmoeConfig, T: int) -> int:
@@ -301,66 +306,68 @@ def smoe_expert_ffn_save(cfg, x, x_perm, row_token, offsets, T, packed, y, gu_q,
                          stream=None):
     """smoe_expert_ffn with the 8-bit checkpoint of the gate and up products (see include/stepmoe.h)."""
     H, I, R = cfg.hidden, cfg.inter, T * cfg.top_k
-    p = _pointers("smoe_expert_ffn_save", T, "x", x, "bfloat16", T * H, "x_perm", x_perm, "bfloat16", R * H,
-                  "row_token", row_token, "int32", R, "offsets", offsets, "int32", cfg.n_experts + 1,
-                  "y", y, "bfloat16", (R + T) * H, "gu_q", gu_q, "uint8", (R + T) * 2 * I,
-                  "gu_scale", gu_scale, "uint8", 2 * I // 32 * (R + T))
-    _check("smoe_expert_ffn_save", lib().smoe_expert_ffn_save(ctypes.byref(cfg), *p[:4], T, _p(packed), *p[4:], _p(ws),
-                                                              _ws_bytes(ws, ws_bytes), _s(stream)))
+    p = _arguments("smoe_expert_ffn_save", T, ws, ws_bytes, stream,
+                   "x", x, "bfloat16", T * H, "x_perm", x_perm, "bfloat16", R * H,
+                   "row_token", row_token, "int32", R, "offsets", offsets, "int32", cfg.n_experts + 1,
+                   "y", y, "bfloat16", (R + T) * H, "gu_q", gu_q, "uint8", (R + T) * 2 * I,
+                   "gu_scale", gu_scale, "uint8", 2 * I // 32 * (R + T))
+    _check("smoe_expert_ffn_save", lib().smoe_expert_ffn_save(ctypes.byref(cfg), *p[:4], T, _p(packed), *p[4:]))
 
 
 def smoe_checkpoint_values(cfg, gu_q, gu_scale, T, gu, stream=None):
     """The bf16 values a checkpoint stands for."""
     I, rows = cfg.inter, T * cfg.top_k + T
-    p = _pointers("smoe_checkpoint_values", T, "gu_q", gu_q, "uint8", rows * 2 * I,
-                  "gu_scale", gu_scale, "uint8", 2 * I // 32 * rows, "gu", gu, "bfloat16", rows * 2 * I)
-    _check("smoe_checkpoint_values", lib().smoe_checkpoint_values(ctypes.byref(cfg), p[0], p[1], T, p[2], _s(stream)))
+    p = _arguments("smoe_checkpoint_values", T, None, None, stream,
+                   "gu_q", gu_q, "uint8", rows * 2 * I,
+                   "gu_scale", gu_scale, "uint8", 2 * I // 32 * rows, "gu", gu, "bfloat16", rows * 2 * I)
+    _check("smoe_checkpoint_values", lib().smoe_checkpoint_values(ctypes.byref(cfg), p[0], p[1], T, p[2], p[5]))
 
 
 def smoe_combine_backward(cfg, dout, y, perm_row, topk_w, T, dy, dtopk_w, ws=None, ws_bytes=None, stream=None):
     H, R = cfg.hidden, T * cfg.top_k
-    p = _pointers("smoe_combine_backward", T, "dout", dout, "bfloat16", T * H, "y", y, "bfloat16", (R + T) * H,
-                  "perm_row", perm_row, "int32", R, "topk_w", topk_w, "float32", R, "dy", dy, "bfloat16", R * H,
-                  "dtopk_w", dtopk_w, "float32", R)
-    _check("smoe_combine_backward", lib().smoe_combine_backward(ctypes.byref(cfg), *p[:4], T, *p[4:], _p(ws),
-                                                                _ws_bytes(ws, ws_bytes), _s(stream)))
+    p = _arguments("smoe_combine_backward", T, ws, ws_bytes, stream,
+                   "dout", dout, "bfloat16", T * H, "y", y, "bfloat16", (R + T) * H,
+                   "perm_row", perm_row, "int32", R, "topk_w", topk_w, "float32", R, "dy", dy, "bfloat16", R * H,
+                   "dtopk_w", dtopk_w, "float32", R)
+    _check("smoe_combine_backward", lib().smoe_combine_backward(ctypes.byref(cfg), *p[:4], T, *p[4:]))
 
 
 def smoe_route_backward(cfg, x, T, logits, topk_idx, topk_w, dtopk_w, offsets, perm_row, row_token, dlogits, dw_router,
                         ws=None, ws_bytes=None, stream=None):
     H, E, R = cfg.hidden, cfg.n_experts, T * cfg.top_k
-    p = _pointers("smoe_route_backward", T, "x", x, "bfloat16", T * H, "logits", logits, "float32", T * E,
-                  "topk_idx", topk_idx, "int32", R, "topk_w", topk_w, "float32", R,
-                  "dtopk_w", dtopk_w, "float32", R, "offsets", offsets, "int32", E + 1,
-                  "perm_row", perm_row, "int32", R, "row_token", row_token, "int32", R,
-                  "dlogits", dlogits, "float32", R, "dw_router", dw_router, "float32", E * H)
-    _check("smoe_route_backward", lib().smoe_route_backward(ctypes.byref(cfg), p[0], T, *p[1:], _p(ws),
-                                                            _ws_bytes(ws, ws_bytes), _s(stream)))
+    p = _arguments("smoe_route_backward", T, ws, ws_bytes, stream,
+                   "x", x, "bfloat16", T * H, "logits", logits, "float32", T * E,
+                   "topk_idx", topk_idx, "int32", R, "topk_w", topk_w, "float32", R,
+                   "dtopk_w", dtopk_w, "float32", R, "offsets", offsets, "int32", E + 1,
+                   "perm_row", perm_row, "int32", R, "row_token", row_token, "int32", R,
+                   "dlogits", dlogits, "float32", R, "dw_router", dw_router, "float32", E * H)
+    _check("smoe_route_backward", lib().smoe_route_backward(ctypes.byref(cfg), p[0], T, *p[1:]))
 
 
 def smoe_expert_ffn_backward(cfg, x, x_perm, offsets, T, packed, gu_q, gu_scale, dy, dout, dx_rows, dw_gate, dw_up,
                              dw_down, dws_gate, dws_up, dws_down, ws=None, ws_bytes=None, stream=None):
     H, E, I, R = cfg.hidden, cfg.n_experts, cfg.inter, T * cfg.top_k
     w = H * I
-    p = _pointers("smoe_expert_ffn_backward", T, "x", x, "bfloat16", T * H, "x_perm", x_perm, "bfloat16", R * H,
-                  "offsets", offsets, "int32", E + 1, "gu_q", gu_q, "uint8", (R + T) * 2 * I,
-                  "gu_scale", gu_scale, "uint8", 2 * I // 32 * (R + T), "dy", dy, "bfloat16", R * H,
-                  "dout", dout, "bfloat16", T * H, "dx_rows", dx_rows, "bfloat16", (R + T) * H,
-                  "dw_gate", dw_gate, "bfloat16", E * w, "dw_up", dw_up, "bfloat16", E * w,
-                  "dw_down", dw_down, "bfloat16", E * w, "dws_gate", dws_gate, "bfloat16", w,
-                  "dws_up", dws_up, "bfloat16", w, "dws_down", dws_down, "bfloat16", w)
-    _check("smoe_expert_ffn_backward", lib().smoe_expert_ffn_backward(ctypes.byref(cfg), *p[:3], T, _p(packed), *p[3:],
-                                                                      _p(ws), _ws_bytes(ws, ws_bytes), _s(stream)))
+    p = _arguments("smoe_expert_ffn_backward", T, ws, ws_bytes, stream,
+                   "x", x, "bfloat16", T * H, "x_perm", x_perm, "bfloat16", R * H,
+                   "offsets", offsets, "int32", E + 1, "gu_q", gu_q, "uint8", (R + T) * 2 * I,
+                   "gu_scale", gu_scale, "uint8", 2 * I // 32 * (R + T), "dy", dy, "bfloat16", R * H,
+                   "dout", dout, "bfloat16", T * H, "dx_rows", dx_rows, "bfloat16", (R + T) * H,
+                   "dw_gate", dw_gate, "bfloat16", E * w, "dw_up", dw_up, "bfloat16", E * w,
+                   "dw_down", dw_down, "bfloat16", E * w, "dws_gate", dws_gate, "bfloat16", w,
+                   "dws_up", dws_up, "bfloat16", w, "dws_down", dws_down, "bfloat16", w)
+    _check("smoe_expert_ffn_backward", lib().smoe_expert_ffn_backward(ctypes.byref(cfg), *p[:3], T, _p(packed), *p[3:]))
 
 
 def smoe_permute_backward(cfg, dx_rows, perm_row, topk_idx, dlogits, w_router, T, dx, ws=None, ws_bytes=None,
                           stream=None):
     H, E, R = cfg.hidden, cfg.n_experts, T * cfg.top_k
-    p = _pointers("smoe_permute_backward", T, "dx_rows", dx_rows, "bfloat16", (R + T) * H,
-                  "perm_row", perm_row, "int32", R, "topk_idx", topk_idx, "int32", R,
-                  "dlogits", dlogits, "float32", R, "w_router", w_router, "float32", E * H, "dx", dx, "bfloat16", T * H)
-    _check("smoe_permute_backward", lib().smoe_permute_backward(ctypes.byref(cfg), *p[:5], T, p[5], _p(ws),
-                                                                _ws_bytes(ws, ws_bytes), _s(stream)))
+    p = _arguments("smoe_permute_backward", T, ws, ws_bytes, stream,
+                   "dx_rows", dx_rows, "bfloat16", (R + T) * H,
+                   "perm_row", perm_row, "int32", R, "topk_idx", topk_idx, "int32", R,
+                   "dlogits", dlogits, "float32", R, "w_router", w_router, "float32", E * H,
+                   "dx", dx, "bfloat16", T * H)
+    _check("smoe_permute_backward", lib().smoe_permute_backward(ctypes.byref(cfg), *p[:5], T, *p[5:]))
 
 
 def smoe_selftest_swiglu(g, u, n, out, stream=None) -> None:
@@ -480,7 +487,8 @@ class MoELayer:
         if ws is None:
             ws = workspace(cfg, T, device=x.device, backward=True)
         s = {"x": x, "topk_idx": new(T, k, dtype=torch.int32), "topk_w": new(T, k, dtype=torch.float32),
-             "logits": new(T, E, dtype=torch.float32), "offsets": torch.zeros(E + 1, dtype=torch.int32, device=x.device),
+             "logits": new(T, E, dtype=torch.float32),
+             "offsets": torch.zeros(E + 1, dtype=torch.int32, device=x.device),
              "perm_row": new(R, dtype=torch.int32), "row_token": new(R, dtype=torch.int32), "x_perm": new(R, H),
              "y": new(R + T, H), "gu_q": new(R + T, 2 * I, dtype=torch.uint8),
              "gu_scale": new(2 * I // 32, R + T, dtype=torch.uint8)}
@@ -509,13 +517,13 @@ class MoELayer:
         at = dict(ws=ws, stream=stream)
         dy, dtopk_w, dlogits = new(R, H), new(T, k, dtype=torch.float32), new(T, k, dtype=torch.float32)
         dx_rows = new(R + T, H)
-        g = {"dx": new(T, H), "dw_router": new(E, H, dtype=torch.float32), "dw_gate": new(E, I, H), "dw_up": new(E, I, H),
-             "dw_down": new(E, H, I), "dws_gate": new(I, H), "dws_up": new(I, H), "dws_down": new(H, I)}
+        g = {"dx": new(T, H), "dw_router": new(E, H, dtype=torch.float32), "dw_gate": new(E, I, H),
+             "dw_up": new(E, I, H), "dw_down": new(E, H, I), "dws_gate": new(I, H), "dws_up": new(I, H), "dws_down": new(H, I)}
         smoe_combine_backward(cfg, dout, s["y"], s["perm_row"], s["topk_w"], T, dy, dtopk_w, **at)
-        smoe_expert_ffn_backward(cfg, s["x"], s["x_perm"], s["offsets"], T, self.packed, s["gu_q"], s["gu_scale"], dy, dout,
-                                 dx_rows, g["dw_gate"], g["dw_up"], g["dw_down"], g["dws_gate"], g["dws_up"],
+        smoe_expert_ffn_backward(cfg, s["x"], s["x_perm"], s["offsets"], T, self.packed, s["gu_q"], s["gu_scale"], dy,
+                                 dout, dx_rows, g["dw_gate"], g["dw_up"], g["dw_down"], g["dws_gate"], g["dws_up"],
                                  g["dws_down"], **at)
-        smoe_route_backward(cfg, s["x"], T, s["logits"], s["topk_idx"], s["topk_w"], dtopk_w, s["offsets"], s["perm_row"],
-                            s["row_token"], dlogits, g["dw_router"], **at)
+        smoe_route_backward(cfg, s["x"], T, s["logits"], s["topk_idx"], s["topk_w"], dtopk_w, s["offsets"],
+                            s["perm_row"], s["row_token"], dlogits, g["dw_router"], **at)
         smoe_permute_backward(cfg, dx_rows, s["perm_row"], s["topk_idx"], dlogits, self.w_router, T, g["dx"], **at)
         return g

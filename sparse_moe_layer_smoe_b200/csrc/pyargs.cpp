@@ -1,12 +1,14 @@
-// The Python binding's argument check, natively: pointers(fn, T, name, tensor, dtype, n, ...) returns the
-// tensors' device pointers, as the function of the same name in __init__.py does in 0.5 us a tensor. It
-// judges only the regular case (a contiguous CUDA tensor of the named type with at least n elements on
-// the current device, an integer, or None); everything else goes to the Python function, which decides
-// and explains.
+// The Python binding's argument check, natively: arguments(fn, T, ws, ws_bytes, stream, name, tensor, dtype, n,
+// ...) returns the tensors' device pointers, then the workspace's pointer and bytes and the stream, as the
+// function of the same name in __init__.py does at 0.5 us a tensor. It decides only the regular case (a
+// contiguous CUDA tensor of the named type with at least n elements on the current device, an integer, or
+// None; a workspace tensor or None, its own size, the current stream); everything else goes to the Python
+// function, which refuses or accepts it and explains.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 namespace {
@@ -30,30 +32,51 @@ bool regular(PyObject* t, PyObject* dtype, int64_t n, int device, PyObject** out
         default: return false;
     }
     if (v.scalar_type() != want || v.layout() != c10::kStrided || v.numel() < n || !v.is_contiguous() || v.is_neg() ||
-        (device >= 0 && (!v.is_cuda() || v.get_device() != device)))
+        !v.is_cuda() || v.get_device() != device)
         return false;
     *out = PyLong_FromVoidPtr(v.data_ptr());
     return *out != nullptr;
 }
 
-PyObject* pointers(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+constexpr Py_ssize_t kHead = 5;   // fn, T, ws, ws_bytes, stream
+
+PyObject* arguments(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     try {
-        if (nargs >= 2 && (nargs - 2) % 4 == 0) {
+        if (nargs >= kHead && (nargs - kHead) % 4 == 0 && args[3] == Py_None && args[4] == Py_None) {
             const int64_t T = PyLong_AsLongLong(args[1]);
-            if (!(T == -1 && PyErr_Occurred())) {
-                const int device = T > 0 ? (int)c10::cuda::current_device() : -1;
-                const Py_ssize_t count = (nargs - 2) / 4;
-                PyObject* list = PyList_New(count);
+            if (T > 0) {
+                const int device = (int)c10::cuda::current_device();
+                const Py_ssize_t count = (nargs - kHead) / 4;
+                PyObject* list = PyList_New(count + 3);
                 if (list == nullptr) return nullptr;
                 bool ok = true;
                 for (Py_ssize_t i = 0; ok && i < count; ++i) {
-                    PyObject* const* a = args + 2 + 4 * i;   // name, tensor, dtype, n
+                    PyObject* const* a = args + kHead + 4 * i;   // name, tensor, dtype, n
                     const int64_t n = PyLong_AsLongLong(a[3]);
                     PyObject* p = nullptr;
                     ok = !(n == -1 && PyErr_Occurred()) && regular(a[1], a[2], n, device, &p);
                     if (ok) PyList_SET_ITEM(list, i, p);
                 }
-                if (ok) return list;
+                int64_t bytes = 0;
+                if (ok && args[2] != Py_None) {
+                    ok = THPVariable_CheckExact(args[2]);
+                    if (ok) {
+                        const at::Tensor& w = THPVariable_Unpack(args[2]);
+                        ok = w.layout() == c10::kStrided && w.is_contiguous() && w.is_cuda() && w.get_device() == device;
+                        if (ok) {
+                            bytes = w.numel() * (int64_t)w.element_size();
+                            PyList_SET_ITEM(list, count, PyLong_FromVoidPtr(w.data_ptr()));
+                        }
+                    }
+                } else if (ok) {
+                    PyList_SET_ITEM(list, count, Py_NewRef(Py_None));
+                }
+                if (ok) {
+                    void* stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream();
+                    PyList_SET_ITEM(list, count + 1, PyLong_FromLongLong(bytes));
+                    PyList_SET_ITEM(list, count + 2, stream ? PyLong_FromVoidPtr(stream) : Py_NewRef(Py_None));
+                    return list;
+                }
                 Py_DECREF(list);
             }
             PyErr_Clear();
@@ -70,7 +93,8 @@ PyObject* use(PyObject*, PyObject* slow) {
 }
 
 PyMethodDef g_methods[] = {
-    {"pointers", (PyCFunction)(void (*)(void))pointers, METH_FASTCALL, "pointers(fn, T, name, tensor, dtype, n, ...) -> list"},
+    {"arguments", (PyCFunction)(void (*)(void))arguments, METH_FASTCALL,
+     "arguments(fn, T, ws, ws_bytes, stream, name, tensor, dtype, n, ...) -> list"},
     {"use", use, METH_O, "use(function): what decides irregular arguments"},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_pyargs", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

@@ -544,6 +544,7 @@ def test_training_step_captured_and_on_another_stream(name):
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
         other = _chain(cfg, x, wr, bias, packed, dout, ws)
+    given = _chain(cfg, x, wr, bias, packed, dout, ws, stream=side)
     torch.cuda.current_stream().wait_stream(side)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
@@ -554,7 +555,7 @@ def test_training_step_captured_and_on_another_stream(name):
         graph.replay()
     torch.cuda.synchronize()
     for key in eager:
-        for got in (other, captured):
+        for got in (other, given, captured):
             assert torch.equal(eager[key].view(torch.uint8), got[key].view(torch.uint8)), key
     # other inputs in the captured tensors
     x.copy_(_bf16(np.random.default_rng(43).normal(size=x.shape))[0])
@@ -683,6 +684,33 @@ def test_no_tokens_give_zero_weight_gradients():
     smoe.smoe_permute_backward(cfg, None, None, None, None, None, 0, None)
     smoe.smoe_expert_ffn_save(cfg, None, None, None, None, 0, None, None, None, None)
     smoe.smoe_checkpoint_values(cfg, None, None, 0, None)
+
+
+def test_native_and_python_arguments_agree():
+    """The native check returns what the Python one does, and leaves to it what is not plain: raw pointers are
+    plain, a stream or a workspace size given by the caller is not."""
+    T = 4
+    ws = torch.zeros(512, dtype=torch.uint8, device="cuda")
+    x, i = torch.zeros(T, 8, dtype=torch.bfloat16, device="cuda"), torch.zeros(T, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    for head in ((T, ws, None, None), (T, None, None, None), (T, ws, 300, None), (T, ws, None, side),
+                 (T, ws.data_ptr(), 512, side.cuda_stream), (0, None, None, None)):
+        args = ("f", *head, "x", x, "bfloat16", T * 8, "none", None, "int32", 1, "raw", x.data_ptr(), "uint8", 1, "i", i,
+                "int32", T)
+        want = smoe._arguments_py(*args)
+        assert smoe._arguments(*args) == want and len(want) == 7
+        assert want[:4] == [x.data_ptr(), None, x.data_ptr(), i.data_ptr()]
+        assert want[6] == (side.cuda_stream if head[3] is not None else torch.cuda.current_stream().cuda_stream or None)
+    with torch.cuda.stream(side):
+        assert smoe._arguments("f", T, ws, None, None)[-1] == side.cuda_stream
+    for bad in (("x", x, "float32", 1), ("x", x, "bfloat16", T * 8 + 1), ("x", x.t(), "bfloat16", 1),
+                ("x", x.cpu(), "bfloat16", 1), ("x", x[:, :4], "bfloat16", 1)):
+        for f in (smoe._arguments, smoe._arguments_py):
+            with pytest.raises(smoe.SmoeError) as ei:
+                f("f", T, ws, None, None, *bad)
+            assert ei.value.status == smoe.SMOE_ERR_INVALID_ARG
+    with pytest.raises(smoe.SmoeError):
+        smoe._arguments("f", T, ws.cpu(), None, None, "x", x, "bfloat16", 1)
 
 
 def test_tensor_checks_of_the_binding():
