@@ -518,7 +518,8 @@ class MoELayer:
         dy, dtopk_w, dlogits = new(R, H), new(T, k, dtype=torch.float32), new(T, k, dtype=torch.float32)
         dx_rows = new(R + T, H)
         g = {"dx": new(T, H), "dw_router": new(E, H, dtype=torch.float32), "dw_gate": new(E, I, H),
-             "dw_up": new(E, I, H), "dw_down": new(E, H, I), "dws_gate": new(I, H), "dws_up": new(I, H), "dws_down": new(H, I)}
+             "dw_up": new(E, I, H), "dw_down": new(E, H, I), "dws_gate": new(I, H), "dws_up": new(I, H),
+             "dws_down": new(H, I)}
         smoe_combine_backward(cfg, dout, s["y"], s["perm_row"], s["topk_w"], T, dy, dtopk_w, **at)
         smoe_expert_ffn_backward(cfg, s["x"], s["x_perm"], s["offsets"], T, self.packed, s["gu_q"], s["gu_scale"], dy,
                                  dout, dx_rows, g["dw_gate"], g["dw_up"], g["dw_down"], g["dws_gate"], g["dws_up"],

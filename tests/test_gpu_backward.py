@@ -36,6 +36,7 @@ SHAPES = {
     "all_experts": (33, 256, 4, 4, 256, False, 0.0),
     "one_slot": (50, 256, 6, 1, 128, False, 0.0),
     "many_slots": (40, 256, 40, 20, 128, False, 0.0),
+    "largest_counts": (70, 128, 1024, 32, 128, False, 0.0),   # the most experts and slots
     "odd_widths": (257, 384, 5, 3, 384, False, 0.0),      # H, I odd multiples of 128, large token tiles
     "pairs": (600, 512, 4, 2, 256, False, 0.0),           # CTA pairs, 256-row tiles
     "pairs_64": (300, 256, 16, 3, 512, True, 0.0),        # CTA pairs, 64-row tiles
@@ -510,6 +511,26 @@ def test_training_step_against_the_oracle(name):
     for key, at in zip(("gate", "up", "down"), dW):
         norm(_np(o["dw_" + key]), at[:E], key)
         norm(_np(o["dws_" + key]), at[E], "shared " + key)
+
+
+def test_kernel_times_and_launch_counts():
+    name = "tiny"
+    T = SHAPES[name][0]
+    packed, W, x, x64, wr, wr64, dout, dout64, bias, _ = _chain_inputs(name, 45)
+    cfg = _cfg(name)
+    layer = smoe.MoELayer(cfg, wr, bias, packed)
+    ws = _ws(cfg, T)
+    smoe.smoe_timing_begin(100)
+    _, saved = layer.forward_train(x, ws)
+    layer.backward(saved, dout, ws)
+    assert smoe.smoe_last_launch_count() == 1      # permute_backward
+    smoe.smoe_checkpoint_values(cfg, saved["gu_q"], saved["gu_scale"], T,
+                                torch.empty(T * cfg.top_k + T, 2 * cfg.inter, dtype=torch.bfloat16, device="cuda"))
+    times = smoe.smoe_timing_end()
+    for kernel in ("expert_gateup_save", "expert_down", "combine_backward", "expert_dh", "expert_dx", "expert_wgrad_down",
+                   "expert_wgrad_gateup", "router_backward", "permute_backward", "checkpoint_values"):
+        launches, ms = times[kernel]
+        assert launches == 1 and 0 < ms < 1000, kernel
 
 
 def test_layer_training_methods_are_the_chain():
