@@ -376,7 +376,7 @@ typedef struct {
                             permute_scatter, gather_rows, expert_gateup, expert_down, combine,
                             pack_gateup, pack_down, router_split, router_gemm, diag,
                             quantize_x, quantize_h, pack_fp8, expert_gateup_save, expert_dh,
-                            expert_dx, expert_wgrad_down, expert_wgrad_gateup, checkpoint_values,
+                            expert_dx, expert_wgrad, checkpoint_values,
                             combine_backward, permute_backward, router_backward,
                             router_wgrad_join */
     int32_t launches;    /* launches recorded */

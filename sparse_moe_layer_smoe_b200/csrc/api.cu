@@ -38,8 +38,8 @@ const char* const kNames[K_NUM_KERNELS] = {"router_logits", "router_topk",   "pe
                                            "pack_gateup",   "pack_down",     "router_split",
                                            "router_gemm",   "diag",        "quantize_x",
                                            "quantize_h",    "pack_fp8",    "expert_gateup_save",
-                                           "expert_dh",     "expert_dx",   "expert_wgrad_down",
-                                           "expert_wgrad_gateup", "checkpoint_values", "combine_backward",
+                                           "expert_dh",     "expert_dx",   "expert_wgrad",
+                                           "checkpoint_values", "combine_backward",
                                            "permute_backward", "router_backward",
                                            "router_wgrad_join"};
 }  // namespace

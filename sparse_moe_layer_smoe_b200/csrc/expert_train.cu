@@ -2,7 +2,7 @@
 // (expert_gemm.cuh, epi_gateup_save), dY the gradient of the expert outputs and F(x) = W_d (SiLU(g) u):
 //   dh = dY W_d;  h, dG, dU from dh, g, u (expert_gemm.cuh, epi_swiglu_backward)       one grouped GEMM
 //   dX = dG W_g + dU W_u                                                                one grouped GEMM
-//   dW_g = dG^T X,  dW_u = dU^T X,  dW_d = dY^T h, for every expert over its own rows   two launches
+//   dW_g = dG^T X,  dW_u = dU^T X,  dW_d = dY^T h, for every expert over its own rows   one launch
 // (SwiGLU experts: Step 3.5 Flash summary, paperlayer.ai, §B.) dh and dx run on the forward pass's
 // kernels and read its packed weights in place, through M-major operand tiles.
 //
@@ -31,22 +31,26 @@ constexpr int kWgStageBytes = 2 * kWgABytes;        // and its half of the colum
 constexpr int kWgMaxStages = 6;
 constexpr int kWgStoreBytes = 32 * 128;   // an epilogue warp's staging box (two each): 32 gradient rows x 64 columns
 
-struct WgradMaps {
+// A contraction over every group's rows: gradient [M][N] of group g = A_g^T B_g. A launch takes two: gate and
+// up (A = dG | dU, B = X), then down (A = dY, B = h).
+struct WgradProblem {
     // operands [rows][cols] viewed as {64 columns, rows, cols / 64}, box {64, 64, 2}: two M-major tiles a load
     CUtensorMap a, a_sh;        // M side of the routed groups and of the shared one
     CUtensorMap b, b_sh;        // N side
     CUtensorMap out[2];         // gradients [E * M'][N]: rows m < m_split go to out[0], the others to out[1]
     CUtensorMap out_sh[2];      // the shared expert's [M'][N]; boxes of 64 columns x 32 rows
-};
-
-struct WgradParams {
-    const int32_t* offsets;   // [E+1] routed row offsets
-    int E, T, routed_rows;
     int M, N;                 // gradient rows (over both outputs) and columns
     int m_split;              // rows of an output (M or M / 2)
     int a_sh_row, b_sh_row;   // first row of the shared group in a_sh / b_sh
+    int nb, upg;              // column blocks, units of a group
+    uint32_t inv_nb, inv_upg; // 2^32 / those, rounded up
+};
+
+struct WgradParams {
+    WgradProblem prob[2];
+    const int32_t* offsets;   // [E+1] routed row offsets
+    int E, T, routed_rows;
     int stages;               // pipeline depth
-    uint32_t inv_nb, inv_upg; // 2^32 / (column blocks), 2^32 / (units of a group), rounded up
     int32_t* err;
 };
 
@@ -93,7 +97,7 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1)
-expert_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradParams p) {
+expert_wgrad_kernel(const __grid_constant__ WgradParams p) {
     extern __shared__ uint8_t smem_raw[];
     const int S = p.stages;
     uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -117,9 +121,8 @@ expert_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradParams p)
     const int rank = (int)cluster_ctarank();
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
     const int E = p.E;
-    const int MB = (p.M + kWgTile - 1) / kWgTile, NB = (p.N + kWgTile - 1) / kWgTile;
-    const int upg = MB * NB;                 // units of a group
-    const int total = (E + 1) * upg;         // at most 1025 * 256 * 128: fits
+    const int total0 = (E + 1) * p.prob[0].upg;              // at most 1025 * 256 * 128 each: fits
+    const int total = total0 + (E + 1) * p.prob[1].upg;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -163,9 +166,9 @@ expert_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradParams p)
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
-    // unit u: the shared group's first (it has the most rows), then the routed groups in order; the
-    // units of a group run at the same time on neighbouring pairs and share its rows in L2
-    struct WUnit { int g, mb, nb, rows, ncols; };
+    // unit u of a problem: the shared group's first (it has the most rows), then the routed groups in order;
+    // the units of a group run at the same time on neighbouring pairs and share its rows in L2
+    struct WUnit { int prob, g, mb, nb, rows, ncols; };
     // a / b by its rounded-up reciprocal: one too high at most (a < 2^32), which the remainder shows
     auto divide = [](int a, int b, uint32_t inv, int& rest) {
         int q = b == 1 ? a : (int)__umulhi((uint32_t)a, inv);
@@ -178,12 +181,14 @@ expert_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradParams p)
     };
     auto unit_at = [&](int u) {
         WUnit w;
+        w.prob = u >= total0 ? 1 : 0;
+        const WgradProblem& q = p.prob[w.prob];
         int r;
-        const int o = divide(u, upg, p.inv_upg, r);
+        const int o = divide(u - (w.prob ? total0 : 0), q.upg, q.inv_upg, r);
         w.g = o == 0 ? E : o - 1;
-        w.mb = divide(r, NB, p.inv_nb, w.nb);
+        w.mb = divide(r, q.nb, q.inv_nb, w.nb);
         w.rows = group_rows(w.g, E, p.T, offs);
-        w.ncols = min(kWgTile, p.N - w.nb * kWgTile);
+        w.ncols = min(kWgTile, q.N - w.nb * kWgTile);
         return w;
     };
     auto is_tail = [](int rows, int k) { return k + kWgKRows > rows && ((rows - k) & 15) != 0; };
@@ -195,9 +200,6 @@ expert_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradParams p)
         // armed; the phase waits for the arming arrival.
         const bool m_side = warp == 0;
         const uint64_t pol = l2_policy_evict_last();
-        const CUtensorMap* const routed_map = m_side ? &maps.a : &maps.b;
-        const CUtensorMap* const shared_map = m_side ? &maps.a_sh : &maps.b_sh;
-        const int shared_row = m_side ? p.a_sh_row : p.b_sh_row;
         const uint32_t dst0 = smem_u32(tiles) + (m_side ? 0 : kWgABytes);
         const uint32_t full0 = mapa_shared(smem_u32(full), 0), tail0 = mapa_shared(smem_u32(tail_full), rank);
         int stage = 0;
@@ -208,8 +210,9 @@ expert_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradParams p)
             const int u = snake_unit(i, pair, npairs, total);
             if (u < 0) continue;
             const WUnit w = unit_at(u);
-            const CUtensorMap* map = w.g < E ? routed_map : shared_map;
-            const int row = w.g < E ? offs[w.g] : shared_row;
+            const WgradProblem& q = p.prob[w.prob];
+            const CUtensorMap* map = m_side ? (w.g < E ? &q.a : &q.a_sh) : (w.g < E ? &q.b : &q.b_sh);
+            const int row = w.g < E ? offs[w.g] : (m_side ? q.a_sh_row : q.b_sh_row);
             // first 64-column block: past M (zero fill) in the second CTA for an odd last block of M; for an odd
             // last block of N each CTA uses one of the two it loads
             const int blk = m_side ? w.mb * (kWgTile / 64) + 2 * rank : w.nb * (kWgTile / 64) + rank * (w.ncols / 128);
@@ -332,7 +335,7 @@ expert_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradParams p)
     } else if (warp >= 4) {
         // ---------------------------------------------------------------- epilogue: TMEM -> bf16 -> TMA store
         constexpr int G = kWgEpiWarps / 4;
-        const int q = warp & 3, g0 = (warp - 4) >> 2;
+        const int quarter = warp & 3, g0 = (warp - 4) >> 2;
         uint8_t* const stg0 = staging + (warp - 4) * 2 * kWgStoreBytes;
         int buf = 0;
         const uint64_t pol = l2_policy_evict_first();
@@ -342,13 +345,14 @@ expert_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradParams p)
             const int u = snake_unit(i, pair, npairs, total);
             if (u < 0) continue;
             const WUnit w = unit_at(u);
-            const int m = w.mb * kWgTile + rank * 128 + q * 32;
-            const int part = m >= p.m_split ? 1 : 0;
-            const CUtensorMap* om = w.g < E ? &maps.out[part] : &maps.out_sh[part];
-            const int y = (w.g < E ? w.g * p.m_split : 0) + m - part * p.m_split;
+            const WgradProblem& q = p.prob[w.prob];
+            const int m = w.mb * kWgTile + rank * 128 + quarter * 32;
+            const int part = m >= q.m_split ? 1 : 0;
+            const CUtensorMap* om = w.g < E ? &q.out[part] : &q.out_sh[part];
+            const int y = (w.g < E ? w.g * q.m_split : 0) + m - part * q.m_split;
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&tfull[acc]), acc_phase, p.err, abort_flag, true))) break;
             tc_fence_after();
-            const uint32_t t_row = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kWgTile);
+            const uint32_t t_row = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kWgTile);
             // the warp's boxes (64-column boxes g0, g0 + G, ..) into registers first, so that the accumulator
             // goes back before the stores
             constexpr int NBOX = kWgTile / 64 / G;
@@ -377,7 +381,7 @@ expert_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradParams p)
 #pragma unroll
             for (int b = 0; b < NBOX; ++b) {
                 const int c = 64 * (g0 + G * b);
-                if (c >= w.ncols || m >= p.M) break;
+                if (c >= w.ncols || m >= q.M) break;
                 // the store before the last has left this staging buffer
                 uint8_t* stg = stg0 + buf * kWgStoreBytes;
                 buf ^= 1;
@@ -411,12 +415,15 @@ expert_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradParams p)
     }
 }
 
-cudaError_t run_wgrad(const WgradMaps& maps, WgradParams p, KernelId id, int num_sms, cudaStream_t s) {
+cudaError_t run_wgrad(WgradParams& p, int num_sms, cudaStream_t s) {
     p.stages = kWgMaxStages;
     while (p.stages > 2 && wgrad_smem_bytes(p.stages, p.E) > (size_t)max_dynamic_smem()) --p.stages;
-    const uint64_t nb = (uint64_t)((p.N + kWgTile - 1) / kWgTile), upg = nb * ((p.M + kWgTile - 1) / kWgTile);
-    p.inv_nb = (uint32_t)(((1ull << 32) + nb - 1) / nb);   // 0 for 1, which is not divided by
-    p.inv_upg = (uint32_t)(((1ull << 32) + upg - 1) / upg);
+    for (WgradProblem& q : p.prob) {
+        q.nb = (q.N + kWgTile - 1) / kWgTile;
+        q.upg = q.nb * ((q.M + kWgTile - 1) / kWgTile);
+        q.inv_nb = (uint32_t)(((1ull << 32) + q.nb - 1) / q.nb);   // 0 for 1, which is not divided by
+        q.inv_upg = (uint32_t)(((1ull << 32) + q.upg - 1) / q.upg);
+    }
     const size_t smem = wgrad_smem_bytes(p.stages, p.E);
     cudaError_t e = cudaFuncSetAttribute(expert_wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -431,8 +438,8 @@ cudaError_t run_wgrad(const WgradMaps& maps, WgradParams p, KernelId id, int num
         if (e != cudaSuccess) return e;
         max_clusters = n > 0 ? n : 1;
     }
-    LaunchTimer lt(id, s);
-    return launch_pdl(expert_wgrad_kernel, dim3(2 * std::min(num_sms / 2, max_clusters)), dim3(kWgThreads), smem, s, maps, p);
+    LaunchTimer lt(K_EXPERT_WGRAD, s);
+    return launch_pdl(expert_wgrad_kernel, dim3(2 * std::min(num_sms / 2, max_clusters)), dim3(kWgThreads), smem, s, p);
 }
 
 }  // namespace
@@ -451,7 +458,8 @@ cudaError_t launch_expert_ffn_backward(const smoe_config_t& c, const ExpertBackw
     };
 
     GemmMaps m1, m2;
-    WgradMaps wd, wg;
+    WgradParams pw = {};
+    WgradProblem &wg = pw.prob[0], &wd = pw.prob[1];
     // packed weights viewed as rows of 64 columns, loaded in boxes of 64 rows
     if (!make_map(&m1.w, wdn, (uint64_t)(E + 1) * H * (I / 64), 64, 64, BK) || !act_maps(m1.act, b.dy, routed, H) ||
         !act_maps(m1.sh, b.dout, T, H) ||
@@ -484,12 +492,20 @@ cudaError_t launch_expert_ffn_backward(const smoe_config_t& c, const ExpertBackw
                   1, 0, b.dx_rows, nullptr, err};
     e = pairs ? run_gemm_pair<MODE_DX>(m2, p2, num_sms, s) : run_gemm<MODE_DX>(m2, p2, num_sms, s);
     if (e != cudaSuccess) return e;
-    e = run_wgrad(wg, WgradParams{b.offsets, E, (int)T, (int)routed, 2 * I, H, I, (int)routed, 0, 0, 0, 0, err},
-                  K_EXPERT_WGRAD_GATEUP, num_sms, s);
-    if (e != cudaSuccess) return e;
-    e = run_wgrad(wd, WgradParams{b.offsets, E, (int)T, (int)routed, H, I, H, 0, (int)routed, 0, 0, 0, err},
-                  K_EXPERT_WGRAD_DOWN, num_sms, s);
-    if (e == cudaSuccess) launches_add(4);
+    wg.M = 2 * I;
+    wg.N = H;
+    wg.m_split = I;
+    wg.a_sh_row = (int)routed;
+    wd.M = wd.m_split = H;
+    wd.N = I;
+    wd.b_sh_row = (int)routed;
+    pw.offsets = b.offsets;
+    pw.E = E;
+    pw.T = (int)T;
+    pw.routed_rows = (int)routed;
+    pw.err = err;
+    e = run_wgrad(pw, num_sms, s);
+    if (e == cudaSuccess) launches_add(3);
     return e;
 }
 

@@ -82,8 +82,8 @@ void launches_add(int n);
 enum KernelId {
     K_ROUTER_LOGITS = 0, K_ROUTER_TOPK, K_PERMUTE_HIST, K_PERMUTE_SCAN, K_PERMUTE_SCATTER, K_GATHER_ROWS,
     K_EXPERT_GATEUP, K_EXPERT_DOWN, K_COMBINE, K_PACK_GATEUP, K_PACK_DOWN, K_ROUTER_SPLIT, K_ROUTER_GEMM,
-    K_DIAG, K_QUANT_X, K_QUANT_H, K_PACK_FP8, K_EXPERT_GATEUP_SAVE, K_EXPERT_DH, K_EXPERT_DX, K_EXPERT_WGRAD_DOWN,
-    K_EXPERT_WGRAD_GATEUP, K_CHECKPOINT_VALUES, K_COMBINE_BACKWARD, K_PERMUTE_BACKWARD, K_ROUTER_BACKWARD,
+    K_DIAG, K_QUANT_X, K_QUANT_H, K_PACK_FP8, K_EXPERT_GATEUP_SAVE, K_EXPERT_DH, K_EXPERT_DX, K_EXPERT_WGRAD,
+    K_CHECKPOINT_VALUES, K_COMBINE_BACKWARD, K_PERMUTE_BACKWARD, K_ROUTER_BACKWARD,
     K_ROUTER_WGRAD_JOIN, K_NUM_KERNELS
 };
 const char* kernel_name(int id);
