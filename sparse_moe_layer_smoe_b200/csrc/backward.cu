@@ -37,8 +37,8 @@ constexpr int kMaxWarps = 8;
 constexpr int kAhead = 2;      // router rows in flight beside the routed ones (1, 2 and 4 measure the same)
 
 // One CTA per token; a thread owns 8 consecutive features of every row and has all k of them in flight.
-// HBM-bound: 8192 tokens of H = 4096, k = 8 in 186 us, 6.1 TB/s (two CTAs an SM instead of three: 199 us;
-// four spill: 241 us).
+// HBM-bound: 8192 tokens of H = 4096, k = 8 in 178 us, 6.4 TB/s (two CTAs an SM instead of three: 199 us;
+// four spill: 241 us). y is read for the last time and passes through L2 (evict-first: 185 us without).
 __global__ void __launch_bounds__(256, 3) combine_backward_kernel(const uint16_t* __restrict__ dout,
                                                                const uint16_t* __restrict__ y,
                                                                const int32_t* __restrict__ perm_row,
@@ -54,6 +54,7 @@ __global__ void __launch_bounds__(256, 3) combine_backward_kernel(const uint16_t
     const int vec = H / 8;
     const int64_t nrouted = (int64_t)T * k;
     const uint4* d4 = reinterpret_cast<const uint4*>(dout) + (size_t)t * vec;
+    const uint64_t pass = l2_policy_evict_first();
     for (int j0 = 0; j0 < k; j0 += kSlots) {
         const int n = min(kSlots, k - j0);
         if (threadIdx.x < kSlots) {
@@ -78,7 +79,7 @@ __global__ void __launch_bounds__(256, 3) combine_backward_kernel(const uint16_t
             uint4 v[kSlots];
 #pragma unroll
             for (int j = 0; j < kSlots; ++j)
-                if (rows[j] >= 0) v[j] = reinterpret_cast<const uint4*>(y)[(size_t)rows[j] * vec + c];
+                if (rows[j] >= 0) v[j] = ld_global_hint(reinterpret_cast<const uint4*>(y) + (size_t)rows[j] * vec + c, pass);
 #pragma unroll
             for (int j = 0; j < kSlots; ++j)
                 if (rows[j] >= 0) {
