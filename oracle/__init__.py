@@ -7,8 +7,8 @@ The layer's oracle is the plain C++17 program ``smoe_oracle.cpp`` (fp64 loops, s
 std::thread; reached through ``oracle.cpp``), exported here under the layer's function names.
 ``oracle.moe`` is a second, independent restatement in numpy with the same names; the pins in
 ``tests/test_oracle_pins.py`` run against both, and ``tests/test_oracle_cross.py`` checks that
-the two agree. The e4m3 (``oracle.fp8``) and monitoring (``oracle.diag``) extensions are numpy,
-pinned in their own test files.
+the two agree. The e4m3 (``oracle.fp8``), monitoring (``oracle.diag``) and gradient
+(``oracle.backward``) extensions are numpy, pinned in their own test files.
 """
 from . import cpp, moe
 from .cpp import (bf16_to_f64, combine, f32_to_f64, moe_dense_masked, moe_given_selection, moe_sparse, normalise,

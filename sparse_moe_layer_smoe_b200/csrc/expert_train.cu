@@ -61,7 +61,7 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int32_t c0,
                  : "memory");
 }
 
-// Operand map (see WgradMaps) of a bf16 matrix [rows][cols], cols a multiple of 64.
+// Operand map (see WgradProblem) of a bf16 matrix [rows][cols], cols a multiple of 64.
 bool make_wgrad_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
