@@ -253,7 +253,7 @@ def smoe_forward_fp8(cfg, x, T, w_router, bias, packed_fp8, out, ws=None, ws_byt
 _dtypes = {}   # name -> torch dtype, filled on the first checked call
 
 
-def _arguments_py(fn: str, T: int, ws, ws_bytes, stream, *args) -> list:
+def _arguments(fn: str, T: int, ws, ws_bytes, stream, *args) -> list:
     """The pointers of (name, tensor, dtype, n) arguments, given flat, then the workspace's pointer and bytes and the
     stream. A torch tensor must hold at least n elements of that type, contiguous, on the current CUDA device
     (whose current stream the call goes to); the workspace too must be there. Raw pointers and None are passed on
@@ -288,14 +288,20 @@ def _stream_or_default():
     return _s(None) if torch.cuda.is_available() else None
 
 
-def _arguments(fn: str, T: int, *args) -> list:
-    """_arguments_py, from the first call on through the native module."""
-    global _arguments
+_native = None   # the _pyargs module
+
+
+def _load_native():
+    """The training calls in C++ (csrc/pyargs.cpp). Each takes the arguments of the function below of the same
+    name and returns the library's status, or None where it leaves the call to that function."""
+    global _native
     import torch  # noqa: F401  (the module links against its libraries)
     from . import _pyargs
-    _pyargs.use(_arguments_py)
-    _arguments = _pyargs.arguments
-    return _arguments(fn, T, *args)
+    _pyargs.use(*(ctypes.cast(getattr(lib(), f), _vp).value for f in (
+        "smoe_expert_ffn_save", "smoe_checkpoint_values", "smoe_combine_backward", "smoe_route_backward",
+        "smoe_expert_ffn_backward", "smoe_permute_backward")))
+    _native = _pyargs
+    return _pyargs
 
 
 def smoe_backward_bytes(cfg: SmoeConfig, T: int) -> int:
@@ -305,69 +311,94 @@ def smoe_backward_bytes(cfg: SmoeConfig, T: int) -> int:
 def smoe_expert_ffn_save(cfg, x, x_perm, row_token, offsets, T, packed, y, gu_q, gu_scale, ws=None, ws_bytes=None,
                          stream=None):
     """smoe_expert_ffn with the 8-bit checkpoint of the gate and up products (see include/stepmoe.h)."""
-    H, I, R = cfg.hidden, cfg.inter, T * cfg.top_k
-    p = _arguments("smoe_expert_ffn_save", T, ws, ws_bytes, stream,
-                   "x", x, "bfloat16", T * H, "x_perm", x_perm, "bfloat16", R * H,
-                   "row_token", row_token, "int32", R, "offsets", offsets, "int32", cfg.n_experts + 1,
-                   "y", y, "bfloat16", (R + T) * H, "gu_q", gu_q, "uint8", (R + T) * 2 * I,
-                   "gu_scale", gu_scale, "uint8", 2 * I // 32 * (R + T))
-    _check("smoe_expert_ffn_save", lib().smoe_expert_ffn_save(ctypes.byref(cfg), *p[:4], T, _p(packed), *p[4:]))
+    status = (_native or _load_native()).expert_ffn_save(
+        cfg, x, x_perm, row_token, offsets, T, packed, y, gu_q, gu_scale, ws, ws_bytes, stream)
+    if status is None:
+        H, I, R = cfg.hidden, cfg.inter, T * cfg.top_k
+        p = _arguments("smoe_expert_ffn_save", T, ws, ws_bytes, stream,
+                       "x", x, "bfloat16", T * H, "x_perm", x_perm, "bfloat16", R * H,
+                       "row_token", row_token, "int32", R, "offsets", offsets, "int32", cfg.n_experts + 1,
+                       "y", y, "bfloat16", (R + T) * H, "gu_q", gu_q, "uint8", (R + T) * 2 * I,
+                       "gu_scale", gu_scale, "uint8", 2 * I // 32 * (R + T))
+        status = lib().smoe_expert_ffn_save(ctypes.byref(cfg), *p[:4], T, _p(packed), *p[4:])
+    _check("smoe_expert_ffn_save", status)
 
 
 def smoe_checkpoint_values(cfg, gu_q, gu_scale, T, gu, stream=None):
     """The bf16 values a checkpoint stands for."""
-    I, rows = cfg.inter, T * cfg.top_k + T
-    p = _arguments("smoe_checkpoint_values", T, None, None, stream,
-                   "gu_q", gu_q, "uint8", rows * 2 * I,
-                   "gu_scale", gu_scale, "uint8", 2 * I // 32 * rows, "gu", gu, "bfloat16", rows * 2 * I)
-    _check("smoe_checkpoint_values", lib().smoe_checkpoint_values(ctypes.byref(cfg), p[0], p[1], T, p[2], p[5]))
+    status = (_native or _load_native()).checkpoint_values(cfg, gu_q, gu_scale, T, gu, stream)
+    if status is None:
+        I, rows = cfg.inter, T * cfg.top_k + T
+        p = _arguments("smoe_checkpoint_values", T, None, None, stream,
+                       "gu_q", gu_q, "uint8", rows * 2 * I,
+                       "gu_scale", gu_scale, "uint8", 2 * I // 32 * rows, "gu", gu, "bfloat16", rows * 2 * I)
+        status = lib().smoe_checkpoint_values(ctypes.byref(cfg), p[0], p[1], T, p[2], p[5])
+    _check("smoe_checkpoint_values", status)
 
 
 def smoe_combine_backward(cfg, dout, y, perm_row, topk_w, T, dy, dtopk_w, ws=None, ws_bytes=None, stream=None):
-    H, R = cfg.hidden, T * cfg.top_k
-    p = _arguments("smoe_combine_backward", T, ws, ws_bytes, stream,
-                   "dout", dout, "bfloat16", T * H, "y", y, "bfloat16", (R + T) * H,
-                   "perm_row", perm_row, "int32", R, "topk_w", topk_w, "float32", R, "dy", dy, "bfloat16", R * H,
-                   "dtopk_w", dtopk_w, "float32", R)
-    _check("smoe_combine_backward", lib().smoe_combine_backward(ctypes.byref(cfg), *p[:4], T, *p[4:]))
+    status = (_native or _load_native()).combine_backward(
+        cfg, dout, y, perm_row, topk_w, T, dy, dtopk_w, ws, ws_bytes, stream)
+    if status is None:
+        H, R = cfg.hidden, T * cfg.top_k
+        p = _arguments("smoe_combine_backward", T, ws, ws_bytes, stream,
+                       "dout", dout, "bfloat16", T * H, "y", y, "bfloat16", (R + T) * H,
+                       "perm_row", perm_row, "int32", R, "topk_w", topk_w, "float32", R, "dy", dy, "bfloat16", R * H,
+                       "dtopk_w", dtopk_w, "float32", R)
+        status = lib().smoe_combine_backward(ctypes.byref(cfg), *p[:4], T, *p[4:])
+    _check("smoe_combine_backward", status)
 
 
 def smoe_route_backward(cfg, x, T, logits, topk_idx, topk_w, dtopk_w, offsets, perm_row, row_token, dlogits, dw_router,
                         ws=None, ws_bytes=None, stream=None):
-    H, E, R = cfg.hidden, cfg.n_experts, T * cfg.top_k
-    p = _arguments("smoe_route_backward", T, ws, ws_bytes, stream,
-                   "x", x, "bfloat16", T * H, "logits", logits, "float32", T * E,
-                   "topk_idx", topk_idx, "int32", R, "topk_w", topk_w, "float32", R,
-                   "dtopk_w", dtopk_w, "float32", R, "offsets", offsets, "int32", E + 1,
-                   "perm_row", perm_row, "int32", R, "row_token", row_token, "int32", R,
-                   "dlogits", dlogits, "float32", R, "dw_router", dw_router, "float32", E * H)
-    _check("smoe_route_backward", lib().smoe_route_backward(ctypes.byref(cfg), p[0], T, *p[1:]))
+    status = (_native or _load_native()).route_backward(
+        cfg, x, T, logits, topk_idx, topk_w, dtopk_w, offsets, perm_row, row_token, dlogits, dw_router, ws, ws_bytes,
+        stream)
+    if status is None:
+        H, E, R = cfg.hidden, cfg.n_experts, T * cfg.top_k
+        p = _arguments("smoe_route_backward", T, ws, ws_bytes, stream,
+                       "x", x, "bfloat16", T * H, "logits", logits, "float32", T * E,
+                       "topk_idx", topk_idx, "int32", R, "topk_w", topk_w, "float32", R,
+                       "dtopk_w", dtopk_w, "float32", R, "offsets", offsets, "int32", E + 1,
+                       "perm_row", perm_row, "int32", R, "row_token", row_token, "int32", R,
+                       "dlogits", dlogits, "float32", R, "dw_router", dw_router, "float32", E * H)
+        status = lib().smoe_route_backward(ctypes.byref(cfg), p[0], T, *p[1:])
+    _check("smoe_route_backward", status)
 
 
 def smoe_expert_ffn_backward(cfg, x, x_perm, offsets, T, packed, gu_q, gu_scale, dy, dout, dx_rows, dw_gate, dw_up,
                              dw_down, dws_gate, dws_up, dws_down, ws=None, ws_bytes=None, stream=None):
-    H, E, I, R = cfg.hidden, cfg.n_experts, cfg.inter, T * cfg.top_k
-    w = H * I
-    p = _arguments("smoe_expert_ffn_backward", T, ws, ws_bytes, stream,
-                   "x", x, "bfloat16", T * H, "x_perm", x_perm, "bfloat16", R * H,
-                   "offsets", offsets, "int32", E + 1, "gu_q", gu_q, "uint8", (R + T) * 2 * I,
-                   "gu_scale", gu_scale, "uint8", 2 * I // 32 * (R + T), "dy", dy, "bfloat16", R * H,
-                   "dout", dout, "bfloat16", T * H, "dx_rows", dx_rows, "bfloat16", (R + T) * H,
-                   "dw_gate", dw_gate, "bfloat16", E * w, "dw_up", dw_up, "bfloat16", E * w,
-                   "dw_down", dw_down, "bfloat16", E * w, "dws_gate", dws_gate, "bfloat16", w,
-                   "dws_up", dws_up, "bfloat16", w, "dws_down", dws_down, "bfloat16", w)
-    _check("smoe_expert_ffn_backward", lib().smoe_expert_ffn_backward(ctypes.byref(cfg), *p[:3], T, _p(packed), *p[3:]))
+    status = (_native or _load_native()).expert_ffn_backward(
+        cfg, x, x_perm, offsets, T, packed, gu_q, gu_scale, dy, dout, dx_rows, dw_gate, dw_up, dw_down, dws_gate,
+        dws_up, dws_down, ws, ws_bytes, stream)
+    if status is None:
+        H, E, I, R = cfg.hidden, cfg.n_experts, cfg.inter, T * cfg.top_k
+        w = H * I
+        p = _arguments("smoe_expert_ffn_backward", T, ws, ws_bytes, stream,
+                       "x", x, "bfloat16", T * H, "x_perm", x_perm, "bfloat16", R * H,
+                       "offsets", offsets, "int32", E + 1, "gu_q", gu_q, "uint8", (R + T) * 2 * I,
+                       "gu_scale", gu_scale, "uint8", 2 * I // 32 * (R + T), "dy", dy, "bfloat16", R * H,
+                       "dout", dout, "bfloat16", T * H, "dx_rows", dx_rows, "bfloat16", (R + T) * H,
+                       "dw_gate", dw_gate, "bfloat16", E * w, "dw_up", dw_up, "bfloat16", E * w,
+                       "dw_down", dw_down, "bfloat16", E * w, "dws_gate", dws_gate, "bfloat16", w,
+                       "dws_up", dws_up, "bfloat16", w, "dws_down", dws_down, "bfloat16", w)
+        status = lib().smoe_expert_ffn_backward(ctypes.byref(cfg), *p[:3], T, _p(packed), *p[3:])
+    _check("smoe_expert_ffn_backward", status)
 
 
 def smoe_permute_backward(cfg, dx_rows, perm_row, topk_idx, dlogits, w_router, T, dx, ws=None, ws_bytes=None,
                           stream=None):
-    H, E, R = cfg.hidden, cfg.n_experts, T * cfg.top_k
-    p = _arguments("smoe_permute_backward", T, ws, ws_bytes, stream,
-                   "dx_rows", dx_rows, "bfloat16", (R + T) * H,
-                   "perm_row", perm_row, "int32", R, "topk_idx", topk_idx, "int32", R,
-                   "dlogits", dlogits, "float32", R, "w_router", w_router, "float32", E * H,
-                   "dx", dx, "bfloat16", T * H)
-    _check("smoe_permute_backward", lib().smoe_permute_backward(ctypes.byref(cfg), *p[:5], T, *p[5:]))
+    status = (_native or _load_native()).permute_backward(
+        cfg, dx_rows, perm_row, topk_idx, dlogits, w_router, T, dx, ws, ws_bytes, stream)
+    if status is None:
+        H, E, R = cfg.hidden, cfg.n_experts, T * cfg.top_k
+        p = _arguments("smoe_permute_backward", T, ws, ws_bytes, stream,
+                       "dx_rows", dx_rows, "bfloat16", (R + T) * H,
+                       "perm_row", perm_row, "int32", R, "topk_idx", topk_idx, "int32", R,
+                       "dlogits", dlogits, "float32", R, "w_router", w_router, "float32", E * H,
+                       "dx", dx, "bfloat16", T * H)
+        status = lib().smoe_permute_backward(ctypes.byref(cfg), *p[:5], T, *p[5:])
+    _check("smoe_permute_backward", status)
 
 
 def smoe_selftest_swiglu(g, u, n, out, stream=None) -> None:

@@ -707,31 +707,54 @@ def test_no_tokens_give_zero_weight_gradients():
     smoe.smoe_checkpoint_values(cfg, None, None, 0, None)
 
 
-def test_native_and_python_arguments_agree():
-    """The native check returns what the Python one does, and leaves to it what is not plain: raw pointers are
-    plain, a stream or a workspace size given by the caller is not."""
-    T = 4
-    ws = torch.zeros(512, dtype=torch.uint8, device="cuda")
-    x, i = torch.zeros(T, 8, dtype=torch.bfloat16, device="cuda"), torch.zeros(T, dtype=torch.int32, device="cuda")
+class _NothingNative:
+    """Stands in for the native module and leaves every call to Python."""
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
+def test_native_and_python_calls_agree(monkeypatch):
+    """The native calls and the Python ones behind them (taken for whatever is not plain) give the same bits."""
+    name = "tiny"
+    T = SHAPES[name][0]
+    packed, W, x, x64, wr, wr64, dout, dout64, bias, _ = _chain_inputs(name, 46)
+    cfg = _cfg(name)
+    ws = _ws(cfg, T)
+    native = _chain(cfg, x, wr, bias, packed, dout, ws)
+    assert smoe._native is not None
+    monkeypatch.setattr(smoe, "_native", _NothingNative())
+    python = _chain(cfg, x, wr, bias, packed, dout, ws)
+    torch.cuda.synchronize()
+    for key in native:
+        assert torch.equal(native[key].view(torch.uint8), python[key].view(torch.uint8)), key
+
+
+def test_native_calls_leave_what_is_not_plain():
+    T, H, k, E, I = 4, 128, 2, 4, 128
+    cfg = smoe.config(H, E, k, I, I)
+    R = T * k
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")
+    i32 = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")
+    ws = _ws(cfg, T)
+    good = [cfg, bf(T, H), bf(R + T, H), i32(R), torch.zeros(T, k, device="cuda"), T, bf(R, H),
+            torch.zeros(T, k, device="cuda"), ws, None, None]
+    f = smoe._load_native().combine_backward
+    assert f(*good) == smoe.SMOE_OK
+    for at, bad in ((0, 7), (1, bf(T, H).float()), (1, bf(T, H).cpu()), (2, bf(R + T - 1, H)), (3, i32(R).long()),
+                    (4, [1.0]), (5, 0), (5, -1), (5, 1 << 40), (5, 4.0), (6, bf(H, R).t()), (7, bf(T, k)), (8, ws.cpu()),
+                    (9, ws.numel()), (10, torch.cuda.current_stream())):
+        assert f(*good[:at], bad, *good[at + 1:]) is None, at
+    assert f(*good[:-1]) is None
+    # raw pointers and None are plain: the library's own checks answer
+    raw = [a.data_ptr() if isinstance(a, torch.Tensor) and i < 8 else a for i, a in enumerate(good)]
+    assert f(*raw) == smoe.SMOE_OK
+    assert f(*good[:1], None, *good[2:]) == smoe.SMOE_ERR_INVALID_ARG
+    assert f(*good[:8], None, None, None) == smoe.SMOE_ERR_INVALID_ARG
+    assert f(*good[:8], ws[:256], None, None) == smoe.SMOE_ERR_WORKSPACE
     side = torch.cuda.Stream()
-    for head in ((T, ws, None, None), (T, None, None, None), (T, ws, 300, None), (T, ws, None, side),
-                 (T, ws.data_ptr(), 512, side.cuda_stream), (0, None, None, None)):
-        args = ("f", *head, "x", x, "bfloat16", T * 8, "none", None, "int32", 1, "raw", x.data_ptr(), "uint8", 1, "i", i,
-                "int32", T)
-        want = smoe._arguments_py(*args)
-        assert smoe._arguments(*args) == want and len(want) == 7
-        assert want[:4] == [x.data_ptr(), None, x.data_ptr(), i.data_ptr()]
-        assert want[6] == (side.cuda_stream if head[3] is not None else torch.cuda.current_stream().cuda_stream or None)
     with torch.cuda.stream(side):
-        assert smoe._arguments("f", T, ws, None, None)[-1] == side.cuda_stream
-    for bad in (("x", x, "float32", 1), ("x", x, "bfloat16", T * 8 + 1), ("x", x.t(), "bfloat16", 1),
-                ("x", x.cpu(), "bfloat16", 1), ("x", x[:, :4], "bfloat16", 1)):
-        for f in (smoe._arguments, smoe._arguments_py):
-            with pytest.raises(smoe.SmoeError) as ei:
-                f("f", T, ws, None, None, *bad)
-            assert ei.value.status == smoe.SMOE_ERR_INVALID_ARG
-    with pytest.raises(smoe.SmoeError):
-        smoe._arguments("f", T, ws.cpu(), None, None, "x", x, "bfloat16", 1)
+        assert f(*good) == smoe.SMOE_OK
+    torch.cuda.synchronize()
 
 
 def test_tensor_checks_of_the_binding():
