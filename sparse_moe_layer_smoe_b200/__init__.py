@@ -461,6 +461,14 @@ def workspace(cfg: SmoeConfig, T: int, forward: bool = True, device="cuda", fp8:
     return torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
 
 
+def _stream_context(stream):
+    """torch.cuda.stream(stream); stream may be None (the current one) or a raw handle."""
+    import torch
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
 def diag_buffers(cfg: SmoeConfig, T: int, device="cuda") -> dict:
     """Device arrays for smoe_forward_diag's outputs."""
     import torch
@@ -505,8 +513,13 @@ class MoELayer:
         return out
 
     def forward_train(self, x, ws=None, stream=None):
-        """The layer's output, and what backward() needs of this step (in 8 bits: the experts' gate and up
-        products). ws: workspace(cfg, T, backward=True), which steps may share one after another."""
+        """The layer's output for x [T, hidden], and what backward() needs of this step (in 8 bits: the experts'
+        gate and up products). ws: workspace(cfg, T, backward=True), which steps may share one after another.
+        stream: as under torch.cuda.stream(stream), so what is returned belongs to that stream."""
+        with _stream_context(stream):
+            return self._forward_train(x, ws)
+
+    def _forward_train(self, x, ws):
         import torch
         cfg, T = self.cfg, x.shape[0]
         E, k, H, I = cfg.n_experts, cfg.top_k, cfg.hidden, cfg.inter
@@ -515,8 +528,12 @@ class MoELayer:
         def new(*shape, dtype=torch.bfloat16):
             return torch.empty(shape, dtype=dtype, device=x.device)
 
+        if tuple(x.shape) != (T, H):
+            raise SmoeError("forward_train", SMOE_ERR_INVALID_ARG, f"x is {tuple(x.shape)}, not (T, {H})")
         if ws is None:
             ws = workspace(cfg, T, device=x.device, backward=True)
+        _arguments("forward_train", T, ws, None, None, "x", x, "bfloat16", T * H, "w_router", self.w_router, "float32",
+                   E * H, "bias", self.bias, "float32", E, "packed", self.packed, None, 0)
         s = {"x": x, "topk_idx": new(T, k, dtype=torch.int32), "topk_w": new(T, k, dtype=torch.float32),
              "logits": new(T, E, dtype=torch.float32),
              "offsets": torch.zeros(E + 1, dtype=torch.int32, device=x.device),
@@ -524,38 +541,44 @@ class MoELayer:
              "y": new(R + T, H), "gu_q": new(R + T, 2 * I, dtype=torch.uint8),
              "gu_scale": new(2 * I // 32, R + T, dtype=torch.uint8)}
         out, counts = new(T, H), new(E, dtype=torch.int32)
-        at = dict(ws=ws, stream=stream)
-        smoe_route(cfg, x, T, self.w_router, self.bias, s["topk_idx"], s["topk_w"], s["logits"], **at)
-        smoe_permute(cfg, s["topk_idx"], T, x, counts, s["offsets"], s["perm_row"], s["row_token"], s["x_perm"], **at)
+        smoe_route(cfg, x, T, self.w_router, self.bias, s["topk_idx"], s["topk_w"], s["logits"], ws=ws)
+        smoe_permute(cfg, s["topk_idx"], T, x, counts, s["offsets"], s["perm_row"], s["row_token"], s["x_perm"], ws=ws)
         smoe_expert_ffn_save(cfg, x, s["x_perm"], s["row_token"], s["offsets"], T, self.packed, s["y"], s["gu_q"],
-                             s["gu_scale"], **at)
-        smoe_combine(cfg, s["y"], s["perm_row"], s["topk_w"], T, out, **at)
+                             s["gu_scale"], ws=ws)
+        smoe_combine(cfg, s["y"], s["perm_row"], s["topk_w"], T, out, ws=ws)
         return out, s
 
     def backward(self, saved, dout, ws=None, stream=None) -> dict:
         """Gradients of <dout, output> of the step that forward_train saved: dx, dw_router, and the experts'
-        dw_gate, dw_up, dw_down, dws_gate, dws_up, dws_down (layouts of pack_weights' inputs)."""
+        dw_gate, dw_up, dw_down, dws_gate, dws_up, dws_down (layouts of pack_weights' inputs). stream: as in
+        forward_train."""
+        with _stream_context(stream):
+            return self._backward(saved, dout, ws)
+
+    def _backward(self, s, dout, ws):
         import torch
-        cfg, s, T = self.cfg, saved, dout.shape[0]
+        cfg, T = self.cfg, dout.shape[0]
         E, k, H, I = cfg.n_experts, cfg.top_k, cfg.hidden, cfg.inter
         R = T * k
 
         def new(*shape, dtype=torch.bfloat16):
             return torch.empty(shape, dtype=dtype, device=dout.device)
 
+        if dout.shape != s["x"].shape:
+            raise SmoeError("backward", SMOE_ERR_INVALID_ARG,
+                            f"dout is {tuple(dout.shape)}, the saved step's output {tuple(s['x'].shape)}")
         if ws is None:
             ws = workspace(cfg, T, device=dout.device, backward=True)
-        at = dict(ws=ws, stream=stream)
         dy, dtopk_w, dlogits = new(R, H), new(T, k, dtype=torch.float32), new(T, k, dtype=torch.float32)
         dx_rows = new(R + T, H)
         g = {"dx": new(T, H), "dw_router": new(E, H, dtype=torch.float32), "dw_gate": new(E, I, H),
              "dw_up": new(E, I, H), "dw_down": new(E, H, I), "dws_gate": new(I, H), "dws_up": new(I, H),
              "dws_down": new(H, I)}
-        smoe_combine_backward(cfg, dout, s["y"], s["perm_row"], s["topk_w"], T, dy, dtopk_w, **at)
+        smoe_combine_backward(cfg, dout, s["y"], s["perm_row"], s["topk_w"], T, dy, dtopk_w, ws=ws)
         smoe_expert_ffn_backward(cfg, s["x"], s["x_perm"], s["offsets"], T, self.packed, s["gu_q"], s["gu_scale"], dy,
                                  dout, dx_rows, g["dw_gate"], g["dw_up"], g["dw_down"], g["dws_gate"], g["dws_up"],
-                                 g["dws_down"], **at)
+                                 g["dws_down"], ws=ws)
         smoe_route_backward(cfg, s["x"], T, s["logits"], s["topk_idx"], s["topk_w"], dtopk_w, s["offsets"],
-                            s["perm_row"], s["row_token"], dlogits, g["dw_router"], **at)
-        smoe_permute_backward(cfg, dx_rows, s["perm_row"], s["topk_idx"], dlogits, self.w_router, T, g["dx"], **at)
+                            s["perm_row"], s["row_token"], dlogits, g["dw_router"], ws=ws)
+        smoe_permute_backward(cfg, dx_rows, s["perm_row"], s["topk_idx"], dlogits, self.w_router, T, g["dx"], ws=ws)
         return g

@@ -84,3 +84,17 @@ def test_workspace_bytes():
     # h, dg and du of every row
     assert many >= 8192 * 9 * 3 * 1280 * 2
     assert smoe.lib().smoe_backward_bytes(ctypes.byref(c), 4, None) == smoe.SMOE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("shape", [(4, 64), (4, 2, 512), (512,)])
+def test_layer_training_methods_check_shapes(shape):
+    import torch
+    layer = smoe.MoELayer(smoe.config(hidden=512), None, None, None)
+    good, bad = torch.zeros(4, 512, dtype=torch.bfloat16), torch.zeros(shape, dtype=torch.bfloat16)
+    with pytest.raises(smoe.SmoeError, match="x is") as e:
+        layer.forward_train(bad)
+    assert e.value.status == smoe.SMOE_ERR_INVALID_ARG
+    for dout in (bad, good[:3]):
+        with pytest.raises(smoe.SmoeError, match="dout is") as e:
+            layer.backward({"x": good}, dout)
+        assert e.value.status == smoe.SMOE_ERR_INVALID_ARG

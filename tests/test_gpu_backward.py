@@ -587,6 +587,38 @@ def test_training_step_captured_and_on_another_stream(name):
         assert torch.equal(want[key].view(torch.uint8), captured[key].view(torch.uint8)), key
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_layer_training_methods_own_memory_on_the_given_stream(raw):
+    """While the given stream is busy, the current one allocates and fills as much memory as the methods used: it
+    gets none of theirs, which work queued on the given stream still needs."""
+    name = "tiny"
+    T = SHAPES[name][0]
+    packed, W, x, x64, wr, wr64, dout, dout64, bias, _ = _chain_inputs(name, 45)
+    cfg = _cfg(name)
+    layer = smoe.MoELayer(cfg, wr, bias, packed)
+    out, saved = layer.forward_train(x)
+    want = dict(layer.backward(saved, dout), out=out)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    given = side.cuda_stream if raw else side
+
+    def fill():
+        return [torch.zeros(n, dtype=torch.uint8, device="cuda")
+                for n in (4 * cfg.n_experts, _ws(cfg, T).numel(), *(v.numel() * v.element_size() for v in want.values()))
+                for _ in range(4)]
+
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    out, saved = layer.forward_train(x, stream=given)
+    kept = fill()
+    got = dict(layer.backward(saved, dout, stream=given), out=out)
+    kept += fill()
+    torch.cuda.current_stream().wait_stream(side)
+    for key, v in got.items():
+        assert torch.equal(v.view(torch.uint8), want[key].view(torch.uint8)), key
+    assert not any(v.any() for v in kept)
+
+
 # ------------------------------------------------------------------------------ bad data, edges
 def test_bad_rows_are_skipped_and_recorded():
     name = "tiny"
