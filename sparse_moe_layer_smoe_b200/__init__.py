@@ -256,8 +256,8 @@ _dtypes = {}   # name -> torch dtype, filled on the first checked call
 def _arguments(fn: str, T: int, ws, ws_bytes, stream, *args) -> list:
     """The pointers of (name, tensor, dtype, n) arguments, given flat, then the workspace's pointer and bytes and the
     stream. A torch tensor must hold at least n elements of that type, contiguous, on the current CUDA device
-    (whose current stream the call goes to); the workspace too must be there. Raw pointers and None are passed on
-    as they are: the library checks them."""
+    (whose current stream the call goes to); the workspace too must be there. With dtype None the type does not
+    matter and n is in bytes. Raw pointers and None are passed on as they are: the library checks them."""
     if not _dtypes:
         import torch
         _dtypes.update({n: getattr(torch, n) for n in ("bfloat16", "float32", "int32", "uint8")})
@@ -272,14 +272,21 @@ def _arguments(fn: str, T: int, ws, ws_bytes, stream, *args) -> list:
             why = f"{name} is {t.dtype}, not torch.{dtype}"
         elif not t.is_contiguous():
             why = f"{name} is not contiguous"
-        elif t.numel() < n:
+        elif dtype is not None and t.numel() < n:
             why = f"{name} has {t.numel()} elements, {n} are needed"
+        elif dtype is None and t.numel() * t.element_size() < n:
+            why = f"{name} has {t.numel() * t.element_size()} bytes, {n} are needed"
         elif here is not None and t.get_device() != here:
             why = f"{name} is on {t.device}, the call runs on cuda:{here}"
         if why:
             raise SmoeError(fn, SMOE_ERR_INVALID_ARG, why)
         out.append(t.data_ptr())
     return [*out, _ws_bytes(ws, ws_bytes), _s(stream) if T > 0 or stream is not None else _stream_or_default()]
+
+
+def _packed_bytes(cfg) -> int:
+    """smoe_packed_weight_bytes, without its check of the config (which the calls make themselves)."""
+    return (cfg.n_experts + 1) * 3 * cfg.inter * cfg.hidden * 2
 
 
 def _stream_or_default():
@@ -318,9 +325,9 @@ def smoe_expert_ffn_save(cfg, x, x_perm, row_token, offsets, T, packed, y, gu_q,
         p = _arguments("smoe_expert_ffn_save", T, ws, ws_bytes, stream,
                        "x", x, "bfloat16", T * H, "x_perm", x_perm, "bfloat16", R * H,
                        "row_token", row_token, "int32", R, "offsets", offsets, "int32", cfg.n_experts + 1,
-                       "y", y, "bfloat16", (R + T) * H, "gu_q", gu_q, "uint8", (R + T) * 2 * I,
+                       "packed", packed, None, _packed_bytes(cfg), "y", y, "bfloat16", (R + T) * H, "gu_q", gu_q, "uint8", (R + T) * 2 * I,
                        "gu_scale", gu_scale, "uint8", 2 * I // 32 * (R + T))
-        status = lib().smoe_expert_ffn_save(ctypes.byref(cfg), *p[:4], T, _p(packed), *p[4:])
+        status = lib().smoe_expert_ffn_save(ctypes.byref(cfg), *p[:4], T, *p[4:])
     _check("smoe_expert_ffn_save", status)
 
 
@@ -376,13 +383,14 @@ def smoe_expert_ffn_backward(cfg, x, x_perm, offsets, T, packed, gu_q, gu_scale,
         w = H * I
         p = _arguments("smoe_expert_ffn_backward", T, ws, ws_bytes, stream,
                        "x", x, "bfloat16", T * H, "x_perm", x_perm, "bfloat16", R * H,
-                       "offsets", offsets, "int32", E + 1, "gu_q", gu_q, "uint8", (R + T) * 2 * I,
+                       "offsets", offsets, "int32", E + 1, "packed", packed, None, _packed_bytes(cfg),
+                       "gu_q", gu_q, "uint8", (R + T) * 2 * I,
                        "gu_scale", gu_scale, "uint8", 2 * I // 32 * (R + T), "dy", dy, "bfloat16", R * H,
                        "dout", dout, "bfloat16", T * H, "dx_rows", dx_rows, "bfloat16", (R + T) * H,
                        "dw_gate", dw_gate, "bfloat16", E * w, "dw_up", dw_up, "bfloat16", E * w,
                        "dw_down", dw_down, "bfloat16", E * w, "dws_gate", dws_gate, "bfloat16", w,
                        "dws_up", dws_up, "bfloat16", w, "dws_down", dws_down, "bfloat16", w)
-        status = lib().smoe_expert_ffn_backward(ctypes.byref(cfg), *p[:3], T, _p(packed), *p[3:])
+        status = lib().smoe_expert_ffn_backward(ctypes.byref(cfg), *p[:3], T, *p[3:])
     _check("smoe_expert_ffn_backward", status)
 
 
@@ -533,7 +541,7 @@ class MoELayer:
         if ws is None:
             ws = workspace(cfg, T, device=x.device, backward=True)
         _arguments("forward_train", T, ws, None, None, "x", x, "bfloat16", T * H, "w_router", self.w_router, "float32",
-                   E * H, "bias", self.bias, "float32", E, "packed", self.packed, None, 0)
+                   E * H, "bias", self.bias, "float32", E, "packed", self.packed, None, _packed_bytes(cfg))
         s = {"x": x, "topk_idx": new(T, k, dtype=torch.int32), "topk_w": new(T, k, dtype=torch.float32),
              "logits": new(T, E, dtype=torch.float32),
              "offsets": torch.zeros(E + 1, dtype=torch.int32, device=x.device),

@@ -72,9 +72,19 @@ struct Call {
         ok = v.layout() == c10::kStrided && v.is_cuda() && v.get_device() == device && v.is_contiguous() && !v.is_neg();
         return ok ? &v : nullptr;
     }
-    // The pointer of argument o: n elements of the given type (of any type: n < 0).
+    // The pointer of argument o: n elements of the given type.
     template <class P>
     P* at(PyObject* o, c10::ScalarType type, int64_t n) {
+        return pointer<P>(o, [&](const at::Tensor& v) { return v.scalar_type() == type && v.numel() >= n; });
+    }
+    // The packed weights, of any type: the tensor maps span all of smoe_packed_weight_bytes.
+    const void* packed(PyObject* o) {
+        return pointer<void>(o, [&](const at::Tensor& v) {
+            return v.numel() * (int64_t)v.element_size() >= (E + 1) * 3 * I * H * 2;
+        });
+    }
+    template <class P, class Fits>
+    P* pointer(PyObject* o, Fits fits) {
         if (!ok || o == Py_None) return nullptr;
         if (PyLong_CheckExact(o)) {
             void* p = PyLong_AsVoidPtr(o);
@@ -83,14 +93,13 @@ struct Call {
         }
         const at::Tensor* v = tensor(o);
         if (v == nullptr) return nullptr;
-        ok = n < 0 || (v->scalar_type() == type && v->numel() >= n);
+        ok = fits(*v);
         return ok ? static_cast<P*>(v->data_ptr()) : nullptr;
     }
     smoe_bf16_t* bf16(PyObject* o, int64_t n) { return at<smoe_bf16_t>(o, BF16, n); }
     float* f32(PyObject* o, int64_t n) { return at<float>(o, F32, n); }
     int32_t* i32(PyObject* o, int64_t n) { return at<int32_t>(o, I32, n); }
     uint8_t* u8(PyObject* o, int64_t n) { return at<uint8_t>(o, U8, n); }
-    void* any(PyObject* o) { return at<void>(o, U8, -1); }
 };
 
 // Runs f, which returns the status of a regular call or -1.
@@ -114,7 +123,7 @@ PyObject* expert_ffn_save(ARGS) {
         Call c(a[0], a[5], a[10], a[11], a[12]);
         const auto *x = c.bf16(a[1], c.T * c.H), *x_perm = c.bf16(a[2], c.R * c.H);
         const int32_t *row_token = c.i32(a[3], c.R), *offsets = c.i32(a[4], c.E + 1);
-        const void* packed = c.any(a[6]);
+        const void* packed = c.packed(a[6]);
         smoe_bf16_t* y = c.bf16(a[7], (c.R + c.T) * c.H);
         uint8_t *q = c.u8(a[8], (c.R + c.T) * 2 * c.I), *s = c.u8(a[9], 2 * c.I / 32 * (c.R + c.T));
         return !c.ok ? -1 : (int)g_expert_ffn_save(c.cfg, x, x_perm, row_token, offsets, c.T, packed, y, q, s, c.ws,
@@ -169,7 +178,7 @@ PyObject* expert_ffn_backward(ARGS) {
         const int64_t rows = c.R + c.T, w = c.H * c.I;
         const auto *x = c.bf16(a[1], c.T * c.H), *x_perm = c.bf16(a[2], c.R * c.H);
         const int32_t* offsets = c.i32(a[3], c.E + 1);
-        const void* packed = c.any(a[5]);
+        const void* packed = c.packed(a[5]);
         const uint8_t *q = c.u8(a[6], rows * 2 * c.I), *s = c.u8(a[7], 2 * c.I / 32 * rows);
         const auto *dy = c.bf16(a[8], c.R * c.H), *dout = c.bf16(a[9], c.T * c.H);
         smoe_bf16_t *dx = c.bf16(a[10], rows * c.H), *dg = c.bf16(a[11], c.E * w), *du = c.bf16(a[12], c.E * w),
