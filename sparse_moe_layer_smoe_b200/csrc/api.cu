@@ -6,7 +6,6 @@
 #include <string.h>
 
 #include <algorithm>
-#include <mutex>
 #include <vector>
 
 #include "internal.h"
@@ -15,10 +14,6 @@ namespace smoe {
 
 namespace {
 thread_local int g_launches = 0;
-
-constexpr int kMaxDevices = 64;
-int g_sms[kMaxDevices] = {0};
-std::mutex g_sms_mu;
 }  // namespace
 
 void launches_reset() { g_launches = 0; }
@@ -58,15 +53,12 @@ LaunchTimer::~LaunchTimer() {
 }
 
 int num_sms_current_device() {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 148;
-    std::lock_guard<std::mutex> lk(g_sms_mu);
-    if (g_sms[dev] == 0) {
-        int n = 0;
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
-        g_sms[dev] = n;
-    }
-    return g_sms[dev];
+    static PerDevice sms;
+    const int n = sms.get([](int dev) {
+        int v = 0;
+        return cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? v : 0;
+    });
+    return n > 0 ? n : 148;
 }
 
 WsLayout ws_layout(const smoe_config_t& c, int64_t T, int num_sms) {
@@ -175,7 +167,7 @@ smoe_status_t smoe_check_config(const smoe_config_t* c) {
         !isfinite(c->swiglu_limit_shared))
         return SMOE_ERR_INVALID_ARG;
     if (c->hidden % 128 != 0 || c->inter % 128 != 0 || c->shared_inter != c->inter) return SMOE_ERR_UNSUPPORTED;
-    if (c->n_experts > 1024 || c->top_k > 32 || c->top_k > c->n_experts) return SMOE_ERR_UNSUPPORTED;
+    if (c->n_experts > kMaxExperts || c->top_k > 32 || c->top_k > c->n_experts) return SMOE_ERR_UNSUPPORTED;
     if (c->hidden > 32768 || c->inter > 32768) return SMOE_ERR_UNSUPPORTED;
     return SMOE_OK;
 }

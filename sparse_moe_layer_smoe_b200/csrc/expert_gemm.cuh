@@ -1252,16 +1252,26 @@ bool make_act_maps(CUtensorMap* maps, const void* base, uint64_t rows, uint64_t 
 }
 
 int max_dynamic_smem() {
-    static int v = 0;
-    if (v == 0) {
-        int dev = 0, n = 0;
-        if (cudaGetDevice(&dev) == cudaSuccess &&
-            cudaDeviceGetAttribute(&n, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) == cudaSuccess && n > 0)
-            v = n;
-        else
-            v = 227 * 1024;
-    }
-    return v;
+    static PerDevice smem;
+    const int n = smem.get([](int dev) {
+        int v = 0;
+        return cudaDeviceGetAttribute(&v, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) == cudaSuccess ? v : 0;
+    });
+    return n > 0 ? n : 227 * 1024;
+}
+
+// Pairs of this kernel resident at once (a GPC with an odd number of free SMs cannot host a pair there), at
+// least 1; 0 if the driver does not say.
+template <class Kernel>
+int resident_pairs(PerDevice& known, Kernel* kernel, int threads, int num_sms) {
+    return known.get([&](int) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(num_sms & ~1);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = max_dynamic_smem();
+        int n = 0;
+        return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess ? 0 : std::max(n, 1);
+    });
 }
 
 template <int MODE, bool F8 = false>
@@ -1277,8 +1287,7 @@ cudaError_t run_gemm(const GemmMaps& maps, GemmParams p, int grid, cudaStream_t 
     if (stages < 2) return cudaErrorInvalidConfiguration;
     p.stages = stages;
     const size_t smem = gemm_smem_bytes(stages, sb, p.E, p.max_tiles);
-    cudaError_t e = cudaFuncSetAttribute(expert_gemm_kernel<MODE, BK, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+    cudaError_t e = allow_smem(expert_gemm_kernel<MODE, BK, F8>, max_dynamic_smem());
     if (e != cudaSuccess) return e;
     {
         LaunchTimer lt(mode_kernel<MODE>(), s);
@@ -1314,21 +1323,12 @@ cudaError_t run_gemm_pair(const GemmMaps& maps, GemmParams p, int num_sms, cudaS
     p.stages = stages;
     const size_t smem = gemm_smem_bytes(stages, sb, p.E, p.max_tiles);
     auto kern = expert_gemm_pair_kernel<MODE, BK, F8>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(kern, max_dynamic_smem());
     if (e != cudaSuccess) return e;
-    // pairs resident at once (a GPC with an odd number of free SMs cannot host a pair there)
-    static int max_clusters = 0;   // of this instantiation
-    if (max_clusters == 0) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(num_sms & ~1);
-        cfg.blockDim = dim3(pair_threads<MODE>());
-        cfg.dynamicSmemBytes = smem;
-        int n = 0;
-        e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
-        if (e != cudaSuccess) return e;
-        max_clusters = n > 0 ? n : 1;
-    }
-    const int pairs = std::min(num_sms / 2, max_clusters);
+    static PerDevice resident;   // of this instantiation
+    const int fit = resident_pairs(resident, kern, pair_threads<MODE>(), num_sms);
+    if (fit == 0) return cudaErrorUnknown;
+    const int pairs = std::min(num_sms / 2, fit);
     {
         LaunchTimer lt(mode_kernel<MODE>(), s);
         return launch_pdl(kern, dim3(2 * pairs), dim3(pair_threads<MODE>()), smem, s, maps, p);

@@ -425,21 +425,13 @@ cudaError_t run_wgrad(WgradParams& p, int num_sms, cudaStream_t s) {
         q.inv_upg = (uint32_t)(((1ull << 32) + q.upg - 1) / q.upg);
     }
     const size_t smem = wgrad_smem_bytes(p.stages, p.E);
-    cudaError_t e = cudaFuncSetAttribute(expert_wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(expert_wgrad_kernel, max_dynamic_smem());
     if (e != cudaSuccess) return e;
-    static int max_clusters = 0;   // pairs resident at once
-    if (max_clusters == 0) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(num_sms & ~1);
-        cfg.blockDim = dim3(kWgThreads);
-        cfg.dynamicSmemBytes = smem;
-        int n = 0;
-        e = cudaOccupancyMaxActiveClusters(&n, expert_wgrad_kernel, &cfg);
-        if (e != cudaSuccess) return e;
-        max_clusters = n > 0 ? n : 1;
-    }
+    static PerDevice resident;
+    const int fit = resident_pairs(resident, expert_wgrad_kernel, kWgThreads, num_sms);
+    if (fit == 0) return cudaErrorUnknown;
     LaunchTimer lt(K_EXPERT_WGRAD, s);
-    return launch_pdl(expert_wgrad_kernel, dim3(2 * std::min(num_sms / 2, max_clusters)), dim3(kWgThreads), smem, s, p);
+    return launch_pdl(expert_wgrad_kernel, dim3(2 * std::min(num_sms / 2, fit)), dim3(kWgThreads), smem, s, p);
 }
 
 }  // namespace

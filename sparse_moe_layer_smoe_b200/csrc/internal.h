@@ -5,6 +5,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 #include "../../include/stepmoe.h"
@@ -13,6 +14,7 @@ namespace smoe {
 
 constexpr size_t kAlign = 256;
 constexpr int kPermuteTokensPerBlock = 256;
+constexpr int kMaxExperts = 1024;
 
 inline size_t align_up(size_t v, size_t a = kAlign) { return (v + a - 1) / a * a; }
 
@@ -72,6 +74,33 @@ WsLayout ws_layout(const smoe_config_t& c, int64_t T, int num_sms);
 WsLayout ws_layout_fp8(const smoe_config_t& c, int64_t T, int num_sms);
 
 int num_sms_current_device();
+
+// A positive number of the current device, asked of the driver on first use; 0 if the asking fails. Host
+// threads that meet here ask twice and store the same.
+constexpr int kMaxDevices = 64;
+class PerDevice {
+    std::atomic<int> known_[kMaxDevices] = {};
+
+  public:
+    template <class Ask>
+    int get(Ask ask) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return ask(0);
+        int v = known_[dev].load(std::memory_order_relaxed);
+        if (v <= 0) {
+            v = ask(dev);
+            if (v > 0) known_[dev].store(v, std::memory_order_relaxed);
+        }
+        return v;
+    }
+};
+
+// The limit of a kernel's dynamic shared memory belongs to the process: a call that set it to its own need
+// would lower it between another host thread's setting and launch. So every call sets the kernel's largest.
+template <class Kernel>
+cudaError_t allow_smem(Kernel* kernel, size_t largest) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)largest);
+}
 
 // Per-thread count of kernels enqueued by the last entry point.
 void launches_reset();

@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(TB) permute_scatter_kernel(const int32_t* __re
 // Outputs are identical to the multi-block path.
 constexpr int kSmallThreads = 1024;
 constexpr int kSmallWarps = kSmallThreads / 32;
+constexpr size_t kSmallMaxSmem = 200 * 1024;
 
 __global__ void __launch_bounds__(kSmallThreads) permute_small_kernel(const int32_t* __restrict__ idx, int T, int k,
                                                                       int E, int32_t* __restrict__ counts,
@@ -276,9 +277,9 @@ cudaError_t launch_permute(const smoe_config_t& c, const int32_t* topk_idx, int6
     cudaError_t e;
     int n = 3;
     const size_t small_sm = permute_small_smem(E);
-    if (T <= kSmallThreads && small_sm <= 200 * 1024) {
+    if (T <= kSmallThreads && small_sm <= kSmallMaxSmem) {
         if (small_sm > 48 * 1024) {
-            e = cudaFuncSetAttribute(permute_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)small_sm);
+            e = allow_smem(permute_small_kernel, kSmallMaxSmem);
             if (e != cudaSuccess) return e;
         }
         {
@@ -303,7 +304,7 @@ cudaError_t launch_permute(const smoe_config_t& c, const int32_t* topk_idx, int6
         if (e != cudaSuccess) return e;
         const size_t sm = 2 * WARPS * E * sizeof(uint32_t);
         if (sm > 48 * 1024) {
-            e = cudaFuncSetAttribute(permute_scatter_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+            e = allow_smem(permute_scatter_kernel, 2 * WARPS * kMaxExperts * sizeof(uint32_t));
             if (e != cudaSuccess) return e;
         }
         {
