@@ -1,5 +1,6 @@
 // The training calls of the Python binding, natively: checking the tensors and calling libstepmoe here takes
-// about 0.5 us where the Python functions of the same names (__init__.py) and ctypes take 3. Only the
+// about 0.5 us where the Python functions of the same names (__init__.py) and ctypes take 3. As with ctypes
+// the interpreter lock is released meanwhile: a launch may block (a full queue, a host callback). Only the
 // regular case is decided here: contiguous CUDA tensors of the right types with at least the elements the
 // call touches, on the current device (or integers and None in their places), T > 0, a workspace tensor of
 // its own size, the current stream. Everything else returns None, and the Python function checks, explains
@@ -102,6 +103,17 @@ struct Call {
     uint8_t* u8(PyObject* o, int64_t n) { return at<uint8_t>(o, U8, n); }
 };
 
+// Calls the library for a regular call, without the interpreter lock; -1 for any other.
+template <class F>
+int call(const Call& c, F library) {
+    if (!c.ok) return -1;
+    struct Unlocked {
+        PyThreadState* state = PyEval_SaveThread();
+        ~Unlocked() { PyEval_RestoreThread(state); }
+    } unlocked;
+    return (int)library();
+}
+
 // Runs f, which returns the status of a regular call or -1.
 template <class F>
 PyObject* guarded(Py_ssize_t nargs, Py_ssize_t want, F f) {
@@ -126,8 +138,9 @@ PyObject* expert_ffn_save(ARGS) {
         const void* packed = c.packed(a[6]);
         smoe_bf16_t* y = c.bf16(a[7], (c.R + c.T) * c.H);
         uint8_t *q = c.u8(a[8], (c.R + c.T) * 2 * c.I), *s = c.u8(a[9], 2 * c.I / 32 * (c.R + c.T));
-        return !c.ok ? -1 : (int)g_expert_ffn_save(c.cfg, x, x_perm, row_token, offsets, c.T, packed, y, q, s, c.ws,
-                                                   c.ws_bytes, c.stream);
+        return call(c, [&] {
+            return g_expert_ffn_save(c.cfg, x, x_perm, row_token, offsets, c.T, packed, y, q, s, c.ws, c.ws_bytes, c.stream);
+        });
     });
 }
 
@@ -138,7 +151,7 @@ PyObject* checkpoint_values(ARGS) {
         const int64_t rows = c.R + c.T;
         const uint8_t *q = c.u8(a[1], rows * 2 * c.I), *s = c.u8(a[2], 2 * c.I / 32 * rows);
         smoe_bf16_t* gu = c.bf16(a[4], rows * 2 * c.I);
-        return !c.ok ? -1 : (int)g_checkpoint_values(c.cfg, q, s, c.T, gu, c.stream);
+        return call(c, [&] { return g_checkpoint_values(c.cfg, q, s, c.T, gu, c.stream); });
     });
 }
 
@@ -151,7 +164,9 @@ PyObject* combine_backward(ARGS) {
         const float* w = c.f32(a[4], c.R);
         smoe_bf16_t* dy = c.bf16(a[6], c.R * c.H);
         float* dw = c.f32(a[7], c.R);
-        return !c.ok ? -1 : (int)g_combine_backward(c.cfg, dout, y, perm_row, w, c.T, dy, dw, c.ws, c.ws_bytes, c.stream);
+        return call(c, [&] {
+            return g_combine_backward(c.cfg, dout, y, perm_row, w, c.T, dy, dw, c.ws, c.ws_bytes, c.stream);
+        });
     });
 }
 
@@ -165,8 +180,10 @@ PyObject* route_backward(ARGS) {
         const float *w = c.f32(a[5], c.R), *dw = c.f32(a[6], c.R);
         const int32_t *offsets = c.i32(a[7], c.E + 1), *perm_row = c.i32(a[8], c.R), *row_token = c.i32(a[9], c.R);
         float *dl = c.f32(a[10], c.R), *dwr = c.f32(a[11], c.E * c.H);
-        return !c.ok ? -1 : (int)g_route_backward(c.cfg, x, c.T, logits, idx, w, dw, offsets, perm_row, row_token, dl, dwr,
-                                                  c.ws, c.ws_bytes, c.stream);
+        return call(c, [&] {
+            return g_route_backward(c.cfg, x, c.T, logits, idx, w, dw, offsets, perm_row, row_token, dl, dwr, c.ws, c.ws_bytes,
+                                    c.stream);
+        });
     });
 }
 
@@ -183,8 +200,10 @@ PyObject* expert_ffn_backward(ARGS) {
         const auto *dy = c.bf16(a[8], c.R * c.H), *dout = c.bf16(a[9], c.T * c.H);
         smoe_bf16_t *dx = c.bf16(a[10], rows * c.H), *dg = c.bf16(a[11], c.E * w), *du = c.bf16(a[12], c.E * w),
                     *dd = c.bf16(a[13], c.E * w), *sg = c.bf16(a[14], w), *su = c.bf16(a[15], w), *sd = c.bf16(a[16], w);
-        return !c.ok ? -1 : (int)g_expert_ffn_backward(c.cfg, x, x_perm, offsets, c.T, packed, q, s, dy, dout, dx, dg, du, dd,
-                                                       sg, su, sd, c.ws, c.ws_bytes, c.stream);
+        return call(c, [&] {
+            return g_expert_ffn_backward(c.cfg, x, x_perm, offsets, c.T, packed, q, s, dy, dout, dx, dg, du, dd, sg, su, sd, c.ws,
+                                         c.ws_bytes, c.stream);
+        });
     });
 }
 
@@ -196,7 +215,9 @@ PyObject* permute_backward(ARGS) {
         const int32_t *perm_row = c.i32(a[2], c.R), *idx = c.i32(a[3], c.R);
         const float *dl = c.f32(a[4], c.R), *wr = c.f32(a[5], c.E * c.H);
         smoe_bf16_t* dx = c.bf16(a[7], c.T * c.H);
-        return !c.ok ? -1 : (int)g_permute_backward(c.cfg, rows, perm_row, idx, dl, wr, c.T, dx, c.ws, c.ws_bytes, c.stream);
+        return call(c, [&] {
+            return g_permute_backward(c.cfg, rows, perm_row, idx, dl, wr, c.T, dx, c.ws, c.ws_bytes, c.stream);
+        });
     });
 }
 

@@ -1,4 +1,6 @@
 """The native form of the training calls: what it leaves to Python, and how it calls the library."""
+import ctypes
+
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -22,10 +24,10 @@ def _calls():
     return out
 
 
-def _native(fn, args):
+def _native(fn, args, native=None):
     """The native call's answer: a status, or None where it leaves the call to Python."""
     rest = (None, None) if "ws" in args else (None,)      # ws_bytes, stream
-    return getattr(smoe._load_native(), fn.removeprefix("smoe_"))(host._cfg(), *args.values(), *rest)
+    return getattr(native or smoe._load_native(), fn.removeprefix("smoe_"))(host._cfg(), *args.values(), *rest)
 
 
 @pytest.mark.parametrize("fn", ["smoe_expert_ffn_save", "smoe_expert_ffn_backward"])
@@ -43,3 +45,16 @@ def test_packed_weights_are_checked(fn):
             getattr(smoe, fn)(host._cfg(), **args)
         assert e.value.status == smoe.SMOE_ERR_INVALID_ARG
     torch.cuda.synchronize()
+
+
+def test_the_library_is_called_without_the_interpreter_lock():
+    """A launch may block (a full queue, a host callback that needs the lock): other Python threads go on meanwhile.
+    PyGILState_Check stands in for the library: it answers 1 where the caller holds the lock, and launches nothing."""
+    calls, native = _calls(), smoe._load_native()
+    check = ctypes.cast(ctypes.pythonapi.PyGILState_Check, ctypes.c_void_p).value
+    try:
+        native.use(*[check] * 6)
+        answers = {fn: _native(fn, args, native) for fn, args in calls.items()}
+    finally:
+        smoe._load_native()
+    assert answers == dict.fromkeys(calls, 0)
