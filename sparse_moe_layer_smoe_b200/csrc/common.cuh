@@ -94,15 +94,29 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t byt
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
+// Whose arrivals a wait acquires: those of this CTA (and the async proxy's), or also those that other CTAs of
+// the cluster released at cluster scope.
+enum WaitScope { kCtaScope, kClusterScope };
+
+template <WaitScope SCOPE = kCtaScope>
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.b32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
+    if constexpr (SCOPE == kCtaScope)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.b32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.b32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
     return ok != 0;
 }
 
@@ -110,12 +124,13 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 // SMOE_ERR_TIMEOUT and raising *abort) when the time limit passes. With check_abort, it also
 // returns false as soon as another role of the CTA has raised *abort; drain waits (loads or
 // MMAs still in flight before the CTA exits) pass check_abort = false.
+template <WaitScope SCOPE = kCtaScope>
 __device__ __forceinline__ bool mbar_wait_for(uint32_t bar, uint32_t parity, int32_t* err, volatile int* abort,
                                               bool check_abort, uint64_t limit_ns) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait<SCOPE>(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (mbar_try_wait<SCOPE>(bar, parity)) return true;
         if ((it & 255u) == 0) {
             if (check_abort && *abort) return false;
             if (globaltimer_ns() - t0 > limit_ns) {
@@ -127,9 +142,10 @@ __device__ __forceinline__ bool mbar_wait_for(uint32_t bar, uint32_t parity, int
     }
 }
 
+template <WaitScope SCOPE = kCtaScope>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int32_t* err, volatile int* abort,
                                           bool check_abort) {
-    return mbar_wait_for(bar, parity, err, abort, check_abort, SMOE_WAIT_LIMIT_NS);
+    return mbar_wait_for<SCOPE>(bar, parity, err, abort, check_abort, SMOE_WAIT_LIMIT_NS);
 }
 
 // The two e4m3 codes in the low 16 bits (low byte first) as fp32 (exact).

@@ -11,8 +11,8 @@
 // (boxes of 64 rows x 64 columns) straight from the row-major activations, so nothing is transposed.
 // Every CTA of the pair loads 128 of the block's rows' columns and 128 of its columns': 32 KB a stage for
 // 512 clocks of MMA, where one CTA alone on 128 x 256 loads 48 KB. 8192 tokens of the full layer (2.3 TFLOP,
-// 9.1 GB written) take 2.8 ms in a burst and 3.1 ms at the power limit, as long as the library's batched
-// GEMM on even groups of 256 rows (3.0 ms); one CTA a tile took 3.9 ms.
+// 9.1 GB written) take 3.05 to 3.15 ms in a burst and 3.6 to 3.7 ms at the power limit; the library's batched
+// GEMM on even groups of 256 rows takes 3.0 ms there.
 // A group's rows start anywhere and rarely end on a tile: the last stage also holds rows of the next
 // group, which may be infinite or NaN, so up to the next multiple of 16 they are overwritten with zeros
 // in shared memory and the products beyond are not issued. Groups without rows get zeros.
@@ -29,6 +29,10 @@ constexpr int kWgKRows = 64;         // rows of a pipeline stage
 constexpr int kWgABytes = 2 * kMnBoxBytes;          // this CTA's 128 gradient rows
 constexpr int kWgStageBytes = 2 * kWgABytes;        // and its half of the columns
 constexpr int kWgMaxStages = 6;
+// Stages that a row tail is loaded ahead of its turn. Its clearing, handed over between the CTAs, takes longer than
+// the other rows' landing: 8192 tokens in a burst 3.22 ms at 0, 3.20 at 1, 3.17 at 2, 3.15 at 3 (at the power
+// limit 3.90 and 3.73 at 0 and 3).
+constexpr int kWgAhead = 3;
 constexpr int kWgStoreBytes = 32 * 128;   // an epilogue warp's staging box (two each): 32 gradient rows x 64 columns
 
 // A contraction over every group's rows: gradient [M][N] of group g = A_g^T B_g. A launch takes two: gate and
@@ -89,11 +93,12 @@ size_t wgrad_smem_bytes(int stages, int E) {
            sizeof(uint64_t) * (4 * (size_t)stages + 5) + 16 + sizeof(int32_t) * (size_t)(E + 1);
 }
 
-// Arrive on an mbarrier of the pair's first CTA. What it orders are writes to this CTA's own shared memory,
-// which fence.proxy.async has already made visible to the tensor cores; a release at cluster scope on top
-// measured 1150 clocks.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// Hand-over of a cleared row tail between the pair's CTAs: the first CTA's MMA reads the second one's shared
+// memory, so what the second one wrote there must be ordered across the cluster. The arrival releases at
+// cluster scope and the wait acquires there; fence.proxy.async before the arrival makes the writes
+// visible to the tensor cores.
+__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1)
@@ -191,7 +196,13 @@ expert_wgrad_kernel(const __grid_constant__ WgradParams p) {
         w.ncols = min(kWgTile, q.N - w.nb * kWgTile);
         return w;
     };
-    auto is_tail = [](int rows, int k) { return k + kWgKRows > rows && ((rows - k) & 15) != 0; };
+    // Stages of a unit, and the place of its row tail among their loads (none: -1); the products take it last.
+    // Fewer than S stages ahead, so that the stage is free again before the ring comes round to it.
+    auto stages_of = [](const WUnit& w) { return (w.rows + kWgKRows - 1) / kWgKRows; };
+    auto tail_place = [&](const WUnit& w) {
+        const int n = stages_of(w);
+        return (w.rows & 15) == 0 ? -1 : max(n - 1 - min(kWgAhead, S - 2), 0);
+    };
 
     if ((warp == 0 || warp == 3) && lane == 0) {
         // ---------------------------------------------------------------- TMA producers (both CTAs)
@@ -216,9 +227,11 @@ expert_wgrad_kernel(const __grid_constant__ WgradParams p) {
             // first 64-column block: past M (zero fill) in the second CTA for an odd last block of M; for an odd
             // last block of N each CTA uses one of the two it loads
             const int blk = m_side ? w.mb * (kWgTile / 64) + 2 * rank : w.nb * (kWgTile / 64) + rank * (w.ncols / 128);
-            for (int k = 0; k < w.rows; k += kWgKRows) {
+            const int n = stages_of(w), place = tail_place(w);
+            for (int j = 0; j < n; ++j) {
                 const uint32_t bit = 1u << stage;
-                const bool tail = is_tail(w.rows, k);
+                const bool tail = j == place;
+                const int k = kWgKRows * (tail ? n - 1 : place >= 0 && j > place ? j - 1 : j);
                 ok = mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, p.err, abort_flag, true);
                 if (!ok) break;
                 if (m_side) {
@@ -270,21 +283,33 @@ expert_wgrad_kernel(const __grid_constant__ WgradParams p) {
             if (!ok) break;
             tc_fence_after();
             uint32_t accum = 0;
-            for (int left = w.rows; left > 0; left -= kWgKRows) {
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(full0 + 8 * stage, phase, p.err, abort_flag, true));
+            const int n = stages_of(w), place = tail_place(w);
+            int held = 0, left = w.rows;
+            uint32_t held_phase = 0;
+            for (int j = 0; j < n + (place >= 0 ? 1 : 0); ++j) {
+                if (j == place) {   // the tail's stage: its turn comes last
+                    held = stage;
+                    held_phase = phase;
+                    if (++stage == S) { stage = 0; phase ^= 1u; }
+                    continue;
+                }
+                const bool tail = j == n;
+                const int at = tail ? held : stage;
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(full0 + 8 * at, tail ? held_phase : phase, p.err, abort_flag, true));
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t a = a0 + (uint32_t)stage * (kWgStageBytes >> 4), b = b0 + (uint32_t)stage * (kWgStageBytes >> 4);
+                const uint64_t a = a0 + (uint32_t)at * (kWgStageBytes >> 4), b = b0 + (uint32_t)at * (kWgStageBytes >> 4);
                 if (elect_one()) {
                     umma_f16_ss_pair(d, a, b, idesc, accum);
                     if (left > 16) umma_f16_ss_pair(d, a + (kMnKStep >> 4), b + (kMnKStep >> 4), idesc, 1u);
                     if (left > 32) umma_f16_ss_pair(d, a + 2 * (kMnKStep >> 4), b + 2 * (kMnKStep >> 4), idesc, 1u);
                     if (left > 48) umma_f16_ss_pair(d, a + 3 * (kMnKStep >> 4), b + 3 * (kMnKStep >> 4), idesc, 1u);
-                    umma_commit_pair_both(empty0 + 8 * stage);
+                    umma_commit_pair_both(empty0 + 8 * at);
                 }
                 __syncwarp();
                 accum = 1;
-                if (++stage == S) { stage = 0; phase ^= 1u; }
+                left -= kWgKRows;
+                if (!tail && ++stage == S) { stage = 0; phase ^= 1u; }
             }
             if (!ok) break;
             if (elect_one()) umma_commit_pair_both(tfull0 + 8 * acc);
@@ -307,11 +332,10 @@ expert_wgrad_kernel(const __grid_constant__ WgradParams p) {
             const int u = snake_unit(i, pair, npairs, total);
             if (u < 0) continue;
             const WUnit w = unit_at(u);
-            const int stages = (w.rows + kWgKRows - 1) / kWgKRows;
-            if (stages == 0) continue;
-            const int last = (stage + stages - 1) % S, valid = w.rows - (stages - 1) * kWgKRows;
-            stage = (stage + stages) % S;
-            if ((valid & 15) == 0) continue;
+            const int n = stages_of(w), place = tail_place(w);
+            const int last = (stage + place) % S, valid = w.rows - (n - 1) * kWgKRows;
+            stage = (stage + n) % S;
+            if (place < 0) continue;
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&tail_full[last]), (tail_par >> last) & 1u, p.err, abort_flag, true));
             if (!ok) break;
             tail_par ^= 1u << last;
@@ -324,10 +348,10 @@ expert_wgrad_kernel(const __grid_constant__ WgradParams p) {
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // for the tensor cores
             __syncwarp();
             if (rank != 0) {
-                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tail_ready[last]), 0));
+                if (lane == 0) mbar_arrive_release_cluster(mapa_shared(smem_u32(&tail_ready[last]), 0));
             } else {
                 const uint32_t bar = smem_u32(&tail_ready[last]), par = ((tail_par >> last) & 1u) ^ 1u;
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar, par, p.err, abort_flag, true));
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait<kClusterScope>(bar, par, p.err, abort_flag, true));
                 if (!ok) break;
                 if (lane == 0) mbar_arrive(smem_u32(&full[last]));
             }
