@@ -309,7 +309,9 @@ SMOE_API smoe_status_t smoe_combine_backward(const smoe_config_t* cfg, const smo
  *   logits [T][E] fp32, topk_idx, topk_w [T][k] (all as smoe_route wrote them), dtopk_w [T][k] fp32,
  *   offsets [E+1], perm_row, row_token [T*k] (smoe_permute)
  *   dlogits   [T][k] fp32 out: the gradient of the selected logits (the others' is 0)
- *   dw_router [E][H] fp32 out (0 for an expert without tokens) */
+ *   dw_router [E][H] fp32 out (0 for an expert without tokens)
+ * An entry that smoe_permute skipped (no row, or an expert out of range) gets dlogits 0, is in no row of
+ * dw_router, and sets SMOE_ERR_DEVICE. */
 SMOE_API smoe_status_t smoe_route_backward(const smoe_config_t* cfg, const smoe_bf16_t* x, int64_t T,
                               const float* logits, const int32_t* topk_idx, const float* topk_w,
                               const float* dtopk_w, const int32_t* offsets, const int32_t* perm_row,
@@ -335,8 +337,9 @@ SMOE_API smoe_status_t smoe_expert_ffn_backward(const smoe_config_t* cfg, const 
 /* Gradient of the layer's input, through the experts (smoe_permute) and the router:
  *   dx[t] = dx_rows[T*k + t] + sum_j dx_rows[perm_row[t*k + j]] + sum_j dlogits[t][j] * w_router[topk_idx[t][j]]
  * summed in fp32 and rounded once to bf16. dlogits NULL leaves the router's term out (topk_idx and
- * w_router are then not read and may be NULL too). An index out of range is skipped and sets
- * SMOE_ERR_DEVICE.
+ * w_router are then not read and may be NULL too). A perm_row out of range adds no row, a topk_idx out of
+ * range no router's term, and either sets SMOE_ERR_DEVICE (smoe_route_backward has given the entries that
+ * smoe_permute skipped dlogits 0).
  *   dx_rows [T*k + T][H] bf16, w_router [E][H] fp32, dx [T][H] bf16 out */
 SMOE_API smoe_status_t smoe_permute_backward(const smoe_config_t* cfg, const smoe_bf16_t* dx_rows,
                               const int32_t* perm_row, const int32_t* topk_idx, const float* dlogits,

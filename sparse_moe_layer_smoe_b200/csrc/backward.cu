@@ -262,8 +262,10 @@ __global__ void __launch_bounds__(kRbThreads) router_backward_kernel(
         if (blockIdx.y != 0 || i >= nrouted) return;
         const int64_t t = i / k;
         const int32_t e = topk_idx[i], r = perm_row[i];
-        if (e < 0 || e >= E || r < 0 || r >= nrouted) record_error(err, SMOE_ERR_DEVICE);
-        dlogits[i] = e >= 0 && e < E ? dlogit(topk_w, dtopk_w, t, (int)(i % k), k, logits[t * E + e], inv_c) : 0.f;
+        // an entry without a row is not in dw_router's sums, so its logit has no gradient either
+        const bool has_row = e >= 0 && e < E && r >= 0 && r < nrouted;
+        if (!has_row) record_error(err, SMOE_ERR_DEVICE);
+        dlogits[i] = has_row ? dlogit(topk_w, dtopk_w, t, (int)(i % k), k, logits[t * E + e], inv_c) : 0.f;
         return;
     }
     // find the item: a scan of the experts' item counts, each thread a contiguous range of experts
