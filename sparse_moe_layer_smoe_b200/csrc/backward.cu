@@ -236,8 +236,8 @@ __device__ __forceinline__ float dlogit(const float* __restrict__ w, const float
 constexpr int kRbThreads = 256;   // 8 features a thread: 2048 features a CTA
 constexpr int kRbFlight = 8;      // rows in flight a thread
 
-// One launch for both gradients. Item = up to kRouterItemRows rows of one expert (an expert without rows
-// has one empty item, which writes its zeros). CTA (x, y): for x below the item bound, item x's sum over
+// One launch for both gradients. Item = up to kRouterItemRows rows of one expert, or all of them where the
+// batch has no more tokens than that (an expert without rows has one empty item, which writes its zeros). CTA (x, y): for x below the item bound, item x's sum over
 // its rows in order, for the 2048 features of slice y; it works out its item from the offsets and its
 // rows' dl from the tokens' weights itself, so nothing has to run before it. Above the bound (y = 0):
 // dlogits of 256 entries each. An expert of one item writes dW_r, the others' items partial sums. Rows
@@ -254,6 +254,7 @@ __global__ void __launch_bounds__(kRbThreads) router_backward_kernel(
     __shared__ float g[kRouterItemRows];
     __shared__ int32_t warp_tot[kRbThreads / 32];
     __shared__ int4 found;   // expert, first row, rows, items of the expert
+    const bool whole = T <= kRouterItemRows;   // an expert's rows are one item
     pdl_wait();
     pdl_launch_dependents();
     const int64_t nrouted = (int64_t)T * k;
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(kRbThreads) router_backward_kernel(
         for (int e = e0; e < e1; ++e) {
             const int a = offsets[e], b = offsets[e + 1];
             bad |= a < 0 || b < a || b > nrouted;
-            n += max(1, (b - a + kRouterItemRows - 1) / kRouterItemRows);
+            n += whole ? 1 : max(1, (b - a + kRouterItemRows - 1) / kRouterItemRows);
         }
         bad = __syncthreads_or(bad);   // corrupt offsets: no rows, one empty item each
         if (bad) {
@@ -299,10 +300,10 @@ __global__ void __launch_bounds__(kRbThreads) router_backward_kernel(
         if (item >= first && item < first + n)
             for (int e = e0; e < e1; ++e) {
                 const int a = bad ? 0 : offsets[e], b = bad ? 0 : offsets[e + 1];
-                const int m = max(1, (b - a + kRouterItemRows - 1) / kRouterItemRows);
+                const int m = whole ? 1 : max(1, (b - a + kRouterItemRows - 1) / kRouterItemRows);
                 if (item < first + m) {
                     const int r = (item - first) * kRouterItemRows;
-                    found = make_int4(e, a + r, min(kRouterItemRows, b - a - r), m);
+                    found = make_int4(e, a + r, whole ? b - a : min(kRouterItemRows, b - a - r), m);
                     break;
                 }
                 first += m;
@@ -312,55 +313,60 @@ __global__ void __launch_bounds__(kRbThreads) router_backward_kernel(
     const int4 it = found;
     if (it.x < 0) return;
     static_assert(kRouterItemRows <= kRbThreads, "one row of an item a thread");
-    int my_t = -1;
-    if ((int)threadIdx.x < it.z) {
-        my_t = row_token[it.y + threadIdx.x];
-        tok[threadIdx.x] = my_t >= 0 && my_t < T ? my_t : 0;
-    }
-    __syncthreads();
     const int c = blockIdx.y * kRbThreads + threadIdx.x;   // 8-feature vector
     const int vec = H / 8;
     const uint4* x4 = reinterpret_cast<const uint4*>(x) + c;
-    if ((int)threadIdx.x < it.z) {
-        const int r = it.y + threadIdx.x, t = my_t;
-        float d = 0.f;
-        bool ok = t >= 0 && t < T;
-        if (ok) {
-            int j = -1;
-            for (int q = 0; q < k; ++q)
-                if (perm_row[(int64_t)t * k + q] == r) j = q;
-            ok = j >= 0;
-            if (ok) d = dlogit(topk_w, dtopk_w, t, j, k, logits[(int64_t)t * E + it.x], inv_c);
-        }
-        if (!ok) record_error(err, SMOE_ERR_DEVICE);   // a row that is not its token's
-        g[threadIdx.x] = d;
-    }
-    __syncthreads();
-    if (c >= vec) return;
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-    int r = 0;
-    for (; r + kRbFlight <= it.z; r += kRbFlight) {
-        uint4 v[kRbFlight];
+    for (int row0 = 0; row0 < it.z; row0 += kRouterItemRows) {
+        const int rows = min(kRouterItemRows, it.z - row0);
+        int my_t = -1;
+        if (row0 > 0) __syncthreads();   // the rows before these have been read
+        if ((int)threadIdx.x < rows) {
+            my_t = row_token[it.y + row0 + threadIdx.x];
+            tok[threadIdx.x] = my_t >= 0 && my_t < T ? my_t : 0;
+        }
+        __syncthreads();
+        if ((int)threadIdx.x < rows) {
+            const int r = it.y + row0 + threadIdx.x, t = my_t;
+            float d = 0.f;
+            bool ok = t >= 0 && t < T;
+            if (ok) {
+                int j = -1;
+                for (int q = 0; q < k; ++q)
+                    if (perm_row[(int64_t)t * k + q] == r) j = q;
+                ok = j >= 0;
+                if (ok) d = dlogit(topk_w, dtopk_w, t, j, k, logits[(int64_t)t * E + it.x], inv_c);
+            }
+            if (!ok) record_error(err, SMOE_ERR_DEVICE);   // a row that is not its token's
+            g[threadIdx.x] = d;
+        }
+        __syncthreads();
+        if (c >= vec) continue;
+        int r = 0;
+        for (; r + kRbFlight <= rows; r += kRbFlight) {
+            uint4 v[kRbFlight];
 #pragma unroll
-        for (int q = 0; q < kRbFlight; ++q) v[q] = x4[(size_t)tok[r + q] * vec];
+            for (int q = 0; q < kRbFlight; ++q) v[q] = x4[(size_t)tok[r + q] * vec];
 #pragma unroll
-        for (int q = 0; q < kRbFlight; ++q) {
+            for (int q = 0; q < kRbFlight; ++q) {
+                float f[8];
+                unpack8(v[q], f);
+                const float s = g[r + q];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[i] = fmaf(s, f[i], acc[i]);
+            }
+        }
+        for (; r < rows; ++r) {
             float f[8];
-            unpack8(v[q], f);
-            const float s = g[r + q];
+            unpack8(x4[(size_t)tok[r] * vec], f);
+            const float s = g[r];
 #pragma unroll
             for (int i = 0; i < 8; ++i) acc[i] = fmaf(s, f[i], acc[i]);
         }
     }
-    for (; r < it.z; ++r) {
-        float f[8];
-        unpack8(x4[(size_t)tok[r] * vec], f);
-        const float s = g[r];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = fmaf(s, f[i], acc[i]);
-    }
+    if (c >= vec) return;
     float4* o = reinterpret_cast<float4*>((it.w == 1 ? dw_router + (size_t)it.x * H : partial + (size_t)blockIdx.x * H) + 8 * c);
     o[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
     o[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
@@ -374,6 +380,7 @@ __global__ void __launch_bounds__(256) router_wgrad_join_kernel(const float* __r
     pdl_wait();
     pdl_launch_dependents();
     const int e = blockIdx.x, E = gridDim.x;
+    // only for batches of more than kRouterItemRows tokens, whose items are of that many rows
     const int n = (offsets[e + 1] - offsets[e] + kRouterItemRows - 1) / kRouterItemRows;
     if (n <= 1) return;
     __shared__ int32_t part[8];
@@ -504,7 +511,7 @@ cudaError_t launch_route_backward(const smoe_config_t& c, const RouteBackward& b
     }
     if (e != cudaSuccess) return e;
     launches_add(1);
-    if (T <= kRouterItemRows) return cudaSuccess;   // a token picks an expert once: no expert has a second item
+    if (T <= kRouterItemRows) return cudaSuccess;   // one item an expert
     {
         LaunchTimer lt(K_ROUTER_WGRAD_JOIN, s);
         e = launch_pdl(router_wgrad_join_kernel, dim3(E, (H / 4 + 127) / 128), dim3(256), 0, s, (const float*)b.partial,

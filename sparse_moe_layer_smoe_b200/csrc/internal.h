@@ -211,6 +211,8 @@ struct BwdLayout {
 BwdLayout bwd_layout(const smoe_config_t& c, int64_t T);
 
 // Router weight gradient: rows of an expert are summed in items of at most this many.
+// In a batch of no more tokens an expert has one item, whatever its rows (no more than tokens, unless a
+// caller's own permutation repeats an expert): its gradient needs no joining.
 constexpr int kRouterItemRows = 64;
 inline int64_t router_max_items(int64_t T, int k, int E) { return T * k / kRouterItemRows + E; }
 

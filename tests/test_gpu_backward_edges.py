@@ -66,3 +66,32 @@ def test_skipped_entries_have_no_gradient():
     ref = dxr64[T * k:] + got.sum(1) + router.sum(1)
     terms = np.abs(dxr64[T * k:]) + np.abs(got).sum(1) + np.abs(router).sum(1)
     _within(_np(dx), ref, np.abs(ref) * U + (2 * k + 2) * F * (1 + U) * terms, "dx")
+
+
+@pytest.mark.parametrize("T,k", [(1, 32), (3, 32), (20, 4), (64, 8), (65, 4)])
+def test_route_backward_of_one_expert_in_every_slot(T, k):
+    """A caller's own permutation may give an expert more rows than there are tokens; every gradient is written."""
+    H, E = 128, 40
+    rng = np.random.default_rng(62)
+    cfg = smoe.config(H, E, k, 128, 128, 3.0)
+    idx = np.full((T, k), 5, dtype=np.int32)
+    perm_row = rng.permutation(T * k).astype(np.int32)
+    row_token = np.empty(T * k, dtype=np.int32)
+    row_token[perm_row] = np.arange(T * k) // k
+    offsets = np.where(np.arange(E + 1) > 5, T * k, 0)
+    x, x64 = _bf16(rng.normal(size=(T, H)))
+    logits, l64 = _f32(rng.normal(size=(T, E)))
+    w, w64 = _f32(rng.uniform(0.2, 1.0, size=(T, k)))
+    dw, dw64 = _f32(rng.normal(size=(T, k)))
+    dl, dwr = torch.full((T, k), 7.0, device="cuda"), torch.full((E, H), 7.0, device="cuda")
+    ws = _ws(cfg, T)
+    smoe.smoe_route_backward(cfg, x, T, logits, _i32(idx), w, dw, _i32(offsets), _i32(perm_row), _i32(row_token), dl, dwr,
+                             ws)
+    assert smoe.smoe_get_device_error(ws) == 0
+    rest = 1.0 - moe.sigmoid(l64[:, 5:6])
+    diff = dw64[:, :, None] - dw64[:, None, :]
+    size = w64 * rest * ((w64 / 3.0)[:, None, :] * np.abs(diff)).sum(2)
+    _within(_np(dl), w64 * rest * ((w64 / 3.0)[:, None, :] * diff).sum(2), (k + 12) * F * size, "dlogits")
+    dl64, got = _np(dl), _np(dwr)
+    assert not np.delete(got, 5, axis=0).any()
+    _within(got[5], dl64.sum(1) @ x64, (T * k + 2) * F * (np.abs(dl64).sum(1) @ np.abs(x64)), "dw_router")
