@@ -78,7 +78,7 @@ typedef struct {
  * layers, 7 (routed) and 16 (shared) for the deepest ones; activation clipping against
  * localized activation blow-up, paperlayer.ai summary §4.1.3 and §B). The pages do not spell out
  * the clamp; read here as: with limit L > 0, gate g = min(g, L) and up u = clamp(u, -L, L) before
- * h = SiLU(g) * u. Limits must be finite and >= 0. */
+ * h = SiLU(g) * u, where NaN stays NaN. Limits must be finite and >= 0. */
 
 /* Human-readable name of a status code. Never NULL. */
 SMOE_API const char* smoe_status_string(smoe_status_t status);
@@ -319,7 +319,8 @@ SMOE_API smoe_status_t smoe_route_backward(const smoe_config_t* cfg, const smoe_
                               void* stream);
 
 /* Gradient of the experts: from the checkpoint, h = SiLU(g) u, dh = dy W_d, and with s = sigmoid(g)
- *   dg = dh u s (1 + g (1 - s)),  du = dh g s   (after the SwiGLU clamp; 0 where it cut g or u off)
+ *   dg = dh u s (1 + g (1 - s)),  du = dh g s   (after the SwiGLU clamp; 0 where it cut g or u off,
+ *   or found NaN, which the gradients of the other one, h and dW_d show)
  *   dx = dg W_g + du W_u;   dW_g = dg^T x,  dW_u = du^T x,  dW_d = dy^T h over each expert's rows
  *   x [T][H], x_perm [T*k][H] (smoe_permute), offsets [E+1], packed (smoe_pack_weights),
  *   gu_q, gu_scale (smoe_expert_ffn_save), dy [T*k][H], dout [T][H] (the shared expert's dy)

@@ -148,6 +148,18 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int32_t
     return mbar_wait_for<SCOPE>(bar, parity, err, abort, check_abort, SMOE_WAIT_LIMIT_NS);
 }
 
+// min(v, limit), and v clamped to [-limit, limit] (limit >= 0): NaN where v is NaN, unlike fminf and fmaxf.
+__device__ __forceinline__ float clamp_above(float v, float limit) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(limit));
+    return r;
+}
+__device__ __forceinline__ float clamp_both(float v, float limit) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(clamp_above(v, limit)), "f"(-limit));
+    return r;
+}
+
 // The two e4m3 codes in the low 16 bits (low byte first) as fp32 (exact).
 __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t codes) {
     const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3));

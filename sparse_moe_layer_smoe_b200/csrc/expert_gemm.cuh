@@ -365,11 +365,11 @@ __device__ __forceinline__ void epi_load(uint32_t t_row, int nt_max, int nch, fl
                         u0 *= rs_u * s0;
                         u1 *= rs_u * s1;
                     }
-                    if (lim > 0.0f) {   // SwiGLU clamp: gate from above, up on both sides
-                        v0 = fminf(v0, lim);
-                        v1 = fminf(v1, lim);
-                        u0 = fminf(fmaxf(u0, -lim), lim);
-                        u1 = fminf(fmaxf(u1, -lim), lim);
+                    if (lim > 0.0f) {   // SwiGLU clamp: gate from above, up on both sides; NaN stays NaN
+                        v0 = clamp_above(v0, lim);
+                        v1 = clamp_above(v1, lim);
+                        u0 = clamp_both(u0, lim);
+                        u1 = clamp_both(u1, lim);
                     }
                     v0 = silu_mul(v0, u0);
                     v1 = silu_mul(v1, u1);
@@ -443,8 +443,8 @@ __device__ __forceinline__ void epi_gateup_save(const GemmParams& p, uint32_t t_
             const float2 q = make_float2(g * __uint_as_float((254u - eg) << 23), u * __uint_as_float((254u - eu) << 23));
             const uint32_t two = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
             if (lim > 0.0f) {
-                g = fminf(g, lim);
-                u = fminf(fmaxf(u, -lim), lim);
+                g = clamp_above(g, lim);
+                u = clamp_both(u, lim);
             }
             if (c + j < nvalid) {
                 uint8_t* d = code_g + (size_t)(c + j) * (2 * I);
@@ -463,7 +463,7 @@ __device__ __forceinline__ void epi_gateup_save(const GemmParams& p, uint32_t t_
 // dh epilogue: the SwiGLU's backward. With g, u the checkpoint's values (g' = min(g, L), u' = u clamped
 // to [-L, L] under a clamp), s = sigmoid(g') and the accumulator dh:
 //   h = g' s u',  dg = dh u' s (1 + g' (1 - s)) where g <= L,  du = dh g' s where |u| <= L, else 0
-// computed in fp32 and rounded once to bf16 (h, dg and du are operands of bf16 products next).
+// (a NaN g or u stays NaN in g', u' and what they enter, and has no gradient itself under a clamp), computed in fp32 and rounded once to bf16 (h, dg and du are operands of bf16 products next).
 template <int G>
 __device__ __forceinline__ void epi_swiglu_backward(const GemmParams& p, uint32_t t_row, int nvalid, float lim,
                                                     int64_t row0, int f, int lane, int c0) {
@@ -501,8 +501,8 @@ __device__ __forceinline__ void epi_swiglu_backward(const GemmParams& p, uint32_
                 if (lim > 0.0f) {
                     pass_g = g <= lim;
                     pass_u = fabsf(u) <= lim;
-                    g = fminf(g, lim);
-                    u = fminf(fmaxf(u, -lim), lim);
+                    g = clamp_above(g, lim);
+                    u = clamp_both(u, lim);
                 }
                 const float dh = __uint_as_float(a[j]);
                 const float s = __fdividef(1.0f, 1.0f + __expf(-g));

@@ -95,3 +95,84 @@ def test_route_backward_of_one_expert_in_every_slot(T, k):
     dl64, got = _np(dl), _np(dwr)
     assert not np.delete(got, 5, axis=0).any()
     _within(got[5], dl64.sum(1) @ x64, (T * k + 2) * F * (np.abs(dl64).sum(1) @ np.abs(x64)), "dw_router")
+
+
+# ------------------------------------------------------------------------------ NaN under the SwiGLU clamp
+@pytest.mark.parametrize("name", ["clamp", "pairs_64"])
+def test_a_nan_token_stays_nan_under_the_clamp(name):
+    """The clamp of a NaN product is NaN, as the oracle's: the token's rows of y are NaN, the others' bits the same."""
+    T, H, E, k, I, _, _ = base.SHAPES[name]
+    rng = np.random.default_rng(63)
+    r, cfg = base._routing(name, rng), base._cfg(name)
+    packed, g64, u64, d64 = base._weights(name, rng)
+    x, x_perm, _ = base._x(name, r, rng)
+
+    def run(x, x_perm):
+        n = T * k + T
+        y, y2 = (torch.full((n, H), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        q = torch.empty(n, 2 * I, dtype=torch.uint8, device="cuda")
+        sc = torch.empty(2 * I // 32, n, dtype=torch.uint8, device="cuda")
+        args = (cfg, x, x_perm, _i32(r["row_token"]), _i32(r["offsets"]), T, packed)
+        smoe.smoe_expert_ffn_save(*args, y, q, sc, _ws(cfg, T))
+        smoe.smoe_expert_ffn(*args, y2, smoe.workspace(cfg, T, forward=False))
+        assert torch.equal(y.view(torch.int16), y2.view(torch.int16))
+        return y
+    clean = run(x, x_perm)
+    t = T // 2
+    x[t] = float("nan")
+    rows = torch.from_numpy(np.concatenate([r["row_token"], np.arange(T)]) == t).cuda()
+    x_perm[rows[:T * k]] = float("nan")
+    for given in (x_perm, None):
+        y = run(x, given)
+        assert torch.isnan(y[rows].float()).all()
+        assert torch.equal(y[~rows].view(torch.int16), clean[~rows].view(torch.int16))
+
+
+def test_a_nan_token_stays_nan_under_the_clamp_with_e4m3_experts():
+    T, H, E, k, I, _, _ = base.SHAPES["clamp"]
+    rng = np.random.default_rng(64)
+    cfg = base._cfg("clamp")
+    w = [_bf16(rng.normal(size=s) * 0.05)[0] for s in ((E, I, H), (E, I, H), (E, H, I), (I, H), (I, H), (H, I))]
+    w[0][:, 7] = w[3][7] = float("nan")      # one gate feature of every expert
+    packed = smoe.pack_weights_fp8(cfg, *w)
+    x, (wr, _), (bias, _) = _bf16(rng.normal(size=(T, H)))[0], _f32(rng.normal(size=(E, H))), _f32(np.zeros(E))
+    out = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    smoe.smoe_forward_fp8(cfg, x, T, wr, bias, packed, out, smoe.workspace(cfg, T, fp8=True))
+    assert torch.isnan(out.float()).all()
+
+
+@pytest.mark.parametrize("name", ["clamp", "pairs_64"])
+def test_nan_products_under_the_clamp_in_the_backward_pass(name):
+    """Where the checkpoint holds NaN, h and the gradients that take it in are NaN as in the oracle: a NaN gate reaches
+    h and du (and its own gradient is cut off: 0), a NaN up product h and dg. All others keep their bits."""
+    T, H, E, k, I, _, _ = base.SHAPES[name]
+    p = base._backward_inputs(name, np.random.default_rng(65))
+    clean, ws = base._outputs(p["cfg"], T), _ws(p["cfg"], T)
+    base._ffn_backward(p, T, clean, ws)
+    b = base._bounds(p["r"], T, k)
+    e = int(np.argmax(p["r"]["counts"]))
+    at = [(b[e], 3), (b[e], I + 40), (b[E] + 1, 64), (b[E] + 2, I + 1)]     # row, column of (g, u)
+    for row, col in at:
+        p["q"][row, col] = 0x7F
+        p["held"][row, col] = np.nan
+    out = base._outputs(p["cfg"], T)
+    base._ffn_backward(p, T, out, ws)
+    g64, u64, d64 = p["W"]
+    for grp, keys in ((e, "dw_"), (E, "dws_")):
+        a, z = b[grp], b[grp + 1]
+        dx, *dW = ob.expert_backward(p["rows64"][a:z], p["held"][a:z, :I], p["held"][a:z, I:], p["dy64"][a:z], g64[grp],
+                                     u64[grp], d64[grp], base._limit(name, grp))
+        got = [out["dx_rows"][a:z]] + [out[keys + q] if grp == E else out[keys + q][grp] for q in ("gate", "up", "down")]
+        was = [clean["dx_rows"][a:z]] + [clean[keys + q] if grp == E else clean[keys + q][grp] for q in ("gate", "up", "down")]
+        for key, v, old, ref in zip(("dx", "gate", "up", "down"), got, was, (dx, *dW)):
+            nan = torch.from_numpy(np.isnan(ref)).cuda()
+            # (a NaN up product reaches no gate gradient where the gate itself is cut off)
+            assert nan.any() or key == "gate", key
+            assert torch.equal(torch.isnan(v.float()), nan), (grp, key)
+            if key == "dx":     # the rows without a NaN product are the same
+                same = torch.tensor([i not in [row for row, _ in at] for i in range(a, z)], device="cuda")
+                assert not nan[same].any()
+                assert torch.equal(v[same].view(torch.int16), old[same].view(torch.int16)), (grp, key)
+    others = [i for i in range(E) if i != e]
+    for key in ("dw_gate", "dw_up", "dw_down"):
+        assert torch.equal(out[key][others].view(torch.int16), clean[key][others].view(torch.int16)), key
