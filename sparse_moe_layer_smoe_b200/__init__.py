@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import warnings
 from dataclasses import dataclass
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -295,18 +296,32 @@ def _stream_or_default():
     return _s(None) if torch.cuda.is_available() else None
 
 
-_native = None   # the _pyargs module
+_native = None   # the _pyargs module, or what stands in for it
+
+
+class _LeavesAll:
+    """Stands in for the native module where it cannot be loaded: every call is left to Python."""
+    def __getattr__(self, name):
+        return lambda *args: None
 
 
 def _load_native():
     """The training calls in C++ (csrc/pyargs.cpp). Each takes the arguments of the function below of the same
-    name and returns the library's status, or None where it leaves the call to that function."""
+    name and returns the library's status, or None where it leaves the call to that function. The module is built
+    for one Python and one torch; under others the functions below make the calls, a few us slower."""
     global _native
-    import torch  # noqa: F401  (the module links against its libraries)
-    from . import _pyargs
-    _pyargs.use(*(ctypes.cast(getattr(lib(), f), _vp).value for f in (
+    functions = [ctypes.cast(getattr(lib(), f), _vp).value for f in (
         "smoe_expert_ffn_save", "smoe_checkpoint_values", "smoe_combine_backward", "smoe_route_backward",
-        "smoe_expert_ffn_backward", "smoe_permute_backward")))
+        "smoe_expert_ffn_backward", "smoe_permute_backward")]
+    try:
+        import torch  # noqa: F401  (the module links against its libraries)
+        from . import _pyargs
+    except ImportError as e:
+        warnings.warn(f"the native training calls cannot be loaded ({e}); calling through Python. Rebuild them with "
+                      "sparse_moe_layer_smoe_b200.build.build_pyargs()", RuntimeWarning, stacklevel=3)
+        _native = _LeavesAll()
+        return _native
+    _pyargs.use(*functions)
     _native = _pyargs
     return _pyargs
 

@@ -1,5 +1,8 @@
 """What the Python form of the training calls refuses, on the host: CPU tensors on a pretended device, and a library
 that must not be reached."""
+import sys
+import warnings
+
 import pytest
 import torch
 
@@ -107,3 +110,22 @@ def test_forward_train_checks_the_packed_weights(library):
     with pytest.raises(smoe.SmoeError, match="packed has"):
         layer.forward_train(_new(T, H), ws=_new(256, dtype=torch.uint8))
     assert library.calls == []
+
+
+def test_calls_without_the_native_module(monkeypatch):
+    """Built for another Python or torch it does not load: one warning, and the Python form makes every call."""
+    monkeypatch.setattr(smoe, "_native", None)
+    monkeypatch.setitem(sys.modules, "sparse_moe_layer_smoe_b200._pyargs", None)
+    monkeypatch.delattr(smoe, "_pyargs", raising=False)
+    c = _cfg()
+    with pytest.warns(RuntimeWarning, match="native training calls"):
+        smoe.smoe_combine_backward(c, None, None, None, None, 0, None, None)
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        smoe.smoe_permute_backward(c, None, None, None, None, None, 0, None)
+        smoe.smoe_expert_ffn_save(c, None, None, None, None, 0, None, None, None, None)
+        smoe.smoe_checkpoint_values(c, None, None, 0, None)
+        with pytest.raises(smoe.SmoeError, match="smoe_route_backward"):
+            smoe.smoe_route_backward(c, *[None] * 1, 0, *[None] * 9)
+        with pytest.raises(smoe.SmoeError, match="smoe_expert_ffn_backward"):
+            smoe.smoe_expert_ffn_backward(c, *[None] * 3, 0, *[None] * 12)
