@@ -47,3 +47,33 @@ def test_row_tails_are_cleared_before_the_products_read_them(shape):
         base._ffn_backward(p, T, out, ws)
         for key in ("dw_gate", "dw_up", "dw_down"):
             assert torch.equal(out[key][good].view(torch.int16), clean[key][good].view(torch.int16)), key
+
+
+WIDE = {
+    # the layer's widths: 256 threads a row and several turns of the feature loops, two slices of router features, partial
+    # sums joined in eight column blocks, an odd number of 256-feature blocks, thirteen weight-gradient units a pair
+    "layer": (200, 4096, 3, 2, 1280, False, 0.0),
+    # odd multiples of 128 with a last slice, column block and turn that are partly empty; single CTAs on large tiles
+    "partial_slices": (150, 2176, 5, 2, 384, True, 1.5),
+    # 45 token tiles of two blocks each: a second unit for the CTA pairs of every product, with one accumulator
+    # set (gate/up with the checkpoint) and two (dh, dx)
+    "second_units": (1100, 512, 40, 4, 512, True, 0.0),
+}
+TESTS = {
+    "combine": base.test_combine_backward,
+    "permute": lambda name: base.test_permute_backward(name, True),
+    "permute_without_router": lambda name: base.test_permute_backward(name, False),
+    "route": base.test_route_backward,
+    "ffn_save": lambda name: base.test_expert_ffn_save(name, False),
+    "ffn_save_gathered": lambda name: base.test_expert_ffn_save(name, True),
+    "ffn_backward": base.test_expert_ffn_backward,
+    "training_step": base.test_training_step_against_the_oracle,
+}
+
+
+@pytest.mark.parametrize("test", TESTS)
+@pytest.mark.parametrize("name", WIDE)
+def test_wide(name, test, shape):
+    """The small shapes' tests, their bounds among them."""
+    shape(name, WIDE[name])
+    TESTS[test](name)

@@ -58,3 +58,29 @@ def test_the_library_is_called_without_the_interpreter_lock():
     finally:
         smoe._load_native()
     assert answers == dict.fromkeys(calls, 0)
+
+
+def _arguments():
+    for fn, args in host._calls().items():
+        for a, v in args.items():
+            if isinstance(v, torch.Tensor):
+                yield fn, a
+
+
+@pytest.mark.parametrize("fn,name", list(_arguments()))
+def test_both_forms_refuse_the_same(fn, name):
+    """Every tensor of every call: of one element fewer, with gaps, on the host or (but for the packed weights and
+    the workspace) of another type the native form leaves the call, and the Python form refuses it."""
+    good = _calls()[fn]
+    t = good[name].reshape(-1)
+    bad = {"short": t[:-1], "gaps": t.repeat(2)[::2], "host": t.cpu()}
+    if name not in ("packed", "ws"):
+        bad["type"] = t.to(torch.float64)
+    if name == "ws":    # the library's own check: SMOE_ERR_WORKSPACE
+        del bad["short"]
+    for kind, b in bad.items():
+        args = {**good, name: b}
+        assert _native(fn, args) is None, kind
+        with pytest.raises(smoe.SmoeError, match=rf"\b{name} ") as e:
+            getattr(smoe, fn)(host._cfg(), **args)
+        assert e.value.status == smoe.SMOE_ERR_INVALID_ARG, kind
