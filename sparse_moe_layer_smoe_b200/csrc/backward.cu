@@ -109,8 +109,10 @@ __global__ void __launch_bounds__(256, 3) combine_backward_kernel(const uint16_t
     }
 }
 
-// One token's dx, by the threads of a CTA. rows, experts, dl: 32 slots each (rows -1: none).
-template <bool ROUTER>
+// One token's dx, by the threads of a CTA. rows, experts, dl: 32 slots each (rows, experts -1: none). PADDED:
+// some of the slots that the loop takes have no expert (k no multiple of 8, skipped entries); without that check
+// of every slot 8192 tokens take 128 us instead of 130.4.
+template <bool ROUTER, bool PADDED>
 __device__ __forceinline__ void permute_backward_row(const uint4* __restrict__ rows4, const uint4* __restrict__ own,
                                                      const float* __restrict__ w_router, const int32_t* rows,
                                                      const int32_t* experts, const float* dl, int k, int H,
@@ -133,9 +135,13 @@ __device__ __forceinline__ void permute_backward_row(const uint4* __restrict__ r
                 if (ROUTER) {
 #pragma unroll
                     for (int j = 0; j < kAhead; ++j) {
-                        const float4* w4 = reinterpret_cast<const float4*>(w_router + (size_t)experts[j0 + z + j] * H) + 2 * c;
-                        a[j] = w4[0];
-                        b[j] = w4[1];
+                        const int32_t e = experts[j0 + z + j];
+                        if (PADDED) a[j] = b[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (!PADDED || e >= 0) {
+                            const float4* w4 = reinterpret_cast<const float4*>(w_router + (size_t)e * H) + 2 * c;
+                            a[j] = w4[0];
+                            b[j] = w4[1];
+                        }
                     }
                 }
                 if (z == 0) {
@@ -180,7 +186,7 @@ __global__ void __launch_bounds__(256, 4) permute_backward_kernel(const uint16_t
                                                                int H, uint16_t* __restrict__ dx, int32_t* err) {
     __shared__ int32_t rows[32], experts[32];
     __shared__ float dl[32];
-    __shared__ bool any_expert;
+    __shared__ unsigned with_expert;   // slots, as bits
     pdl_wait();
     pdl_launch_dependents();
     const int t = blockIdx.x;
@@ -206,22 +212,21 @@ __global__ void __launch_bounds__(256, 4) permute_backward_kernel(const uint16_t
             }
         }
         rows[threadIdx.x] = r;
-        // slots past k and skipped entries repeat one of the token's own experts with weight 0, so that the
-        // loop needs no branch and no other expert's weights are read
         const unsigned valid = __ballot_sync(0xFFFFFFFFu, e >= 0);
-        const int32_t own = __shfl_sync(0xFFFFFFFFu, e, valid ? __ffs(valid) - 1 : 0);
-        experts[threadIdx.x] = e >= 0 ? e : own;
+        experts[threadIdx.x] = e;   // -1 past k and for skipped entries: nothing is read, and 0 * 0 added
         dl[threadIdx.x] = g;
-        if (threadIdx.x == 0) any_expert = valid != 0;
+        if (threadIdx.x == 0) with_expert = valid;
     }
     __syncthreads();
     const uint4* rows4 = reinterpret_cast<const uint4*>(dx_rows);
     const uint4* own = rows4 + (size_t)(nrouted + t) * vec;
     uint4* out = reinterpret_cast<uint4*>(dx) + (size_t)t * vec;
-    if (any_expert)   // false without dlogits
-        permute_backward_row<true>(rows4, own, w_router, rows, experts, dl, k, H, out);
+    if (with_expert == 0)   // also without dlogits
+        permute_backward_row<false, false>(rows4, own, w_router, rows, experts, dl, k, H, out);
+    else if (k % kSlots == 0 && __popc(with_expert) == k)
+        permute_backward_row<true, false>(rows4, own, w_router, rows, experts, dl, k, H, out);
     else
-        permute_backward_row<false>(rows4, own, w_router, rows, experts, dl, k, H, out);
+        permute_backward_row<true, true>(rows4, own, w_router, rows, experts, dl, k, H, out);
 }
 
 // dl of entry i = t * k + j, whose selected logit is l.

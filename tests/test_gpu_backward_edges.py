@@ -176,3 +176,23 @@ def test_nan_products_under_the_clamp_in_the_backward_pass(name):
     others = [i for i in range(E) if i != e]
     for key in ("dw_gate", "dw_up", "dw_down"):
         assert torch.equal(out[key][others].view(torch.int16), clean[key][others].view(torch.int16)), key
+
+
+@pytest.mark.parametrize("k", [1, 3, 5, 8])
+def test_permute_backward_with_an_infinite_router_weight(k):
+    """Slots past k (and skipped entries) add nothing: an infinite weight of a token's own expert stays infinite."""
+    T, H, E = 20, 256, 24
+    rng = np.random.default_rng(66)
+    cfg = smoe.config(H, E, k, 128, 128, 3.0)
+    idx = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    perm_row = moe.permute(idx, E)[2]
+    wr = rng.normal(size=(E, H))
+    wr[:, 5], wr[:, 9] = np.inf, -np.inf
+    (wr, wr64), (dl, dl64) = _f32(wr), _f32(np.abs(rng.normal(size=(T, k))) + 0.1)
+    dxr, dxr64 = _bf16(rng.normal(size=(T * k + T, H)))
+    dx = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    smoe.smoe_permute_backward(cfg, dxr, _i32(perm_row), _i32(idx), dl, wr, T, dx, _ws(cfg, T))
+    got, ref = _np(dx), ob.permute_backward(dxr64, perm_row, idx, dl64, wr64)
+    assert (got[:, 5] == np.inf).all() and (got[:, 9] == -np.inf).all()
+    rest = np.isfinite(wr64[0])
+    assert np.isfinite(got[:, rest]).all() and np.isfinite(ref[:, rest]).all()
