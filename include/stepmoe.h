@@ -264,7 +264,8 @@ SMOE_API smoe_status_t smoe_forward_fp8(const smoe_config_t* cfg, const smoe_bf1
  * from them by differentiation). Gradients of bf16 tensors are bf16, those of fp32 tensors fp32; every
  * sum is fp32 in a fixed order and rounded once, so results do not depend on scheduling. What a call
  * writes is overwritten, not added to. Routed rows past offsets[E] (entries that smoe_permute skipped)
- * are neither read nor written. T == 0 sets the weight gradients to zero. Inputs and outputs must not overlap. The workspace of these calls has
+ * are neither read nor written. T == 0 sets the weight gradients to zero. Inputs and outputs must not
+ * overlap. Host threads may call at the same time, each with its own workspace. The workspace of these calls has
  * smoe_backward_bytes bytes; one workspace may serve calls that run one after another (a stream, or a
  * captured graph replayed in stream order), not calls that overlap. Workspace contents are not kept
  * from one call to the next except the error word. */
@@ -281,14 +282,16 @@ SMOE_API smoe_status_t smoe_backward_bytes(const smoe_config_t* cfg, int64_t T, 
  * Codes are rounded to nearest even from the fp32 accumulators, so a value is held to half a step of
  * e4m3 (2^-4 relative, 2^-10 of the scale below 2^-6 of it). An infinite or NaN product is held as
  * such and gives its block b = 247 or 248, in which its finite neighbours are lost (that row's y is
- * infinite or NaN all the same). Other arguments, y and the workspace (smoe_scratch_bytes)
+ * infinite or NaN all the same, unless the SwiGLU clamp cut an infinite product to the limit). A product of
+ * 248 * 2^120 (fp32's last thirty-second) or more rounds to 2^128, which is infinite in fp32 and bf16. Other arguments, y and the workspace (smoe_scratch_bytes)
  * as smoe_expert_ffn; y has the same bits as smoe_expert_ffn's. */
 SMOE_API smoe_status_t smoe_expert_ffn_save(const smoe_config_t* cfg, const smoe_bf16_t* x, const smoe_bf16_t* x_perm,
                               const int32_t* row_token, const int32_t* offsets, int64_t T, const void* packed,
                               smoe_bf16_t* y, uint8_t* gu_q, uint8_t* gu_scale, void* ws, size_t ws_bytes,
                               void* stream);
 
-/* The values a checkpoint stands for: gu [T*k + T][2 I] bf16 out (exact). Needs no workspace. */
+/* The values a checkpoint stands for: gu [T*k + T][2 I] bf16 out (exact, but for what lies below bf16's least
+ * magnitude, 2^-133, or above its largest). Needs no workspace. */
 SMOE_API smoe_status_t smoe_checkpoint_values(const smoe_config_t* cfg, const uint8_t* gu_q, const uint8_t* gu_scale,
                               int64_t T, smoe_bf16_t* gu, void* stream);
 

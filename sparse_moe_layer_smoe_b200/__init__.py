@@ -537,7 +537,7 @@ class MoELayer:
 
     def forward_train(self, x, ws=None, stream=None):
         """The layer's output for x [T, hidden], and what backward() needs of this step (in 8 bits: the experts'
-        gate and up products). ws: workspace(cfg, T, backward=True), which steps may share one after another.
+        gate and up products; x itself, which like the layer's weights must stay as it is until then). ws: workspace(cfg, T, backward=True), which steps may share one after another.
         stream: as under torch.cuda.stream(stream), so what is returned belongs to that stream."""
         with _stream_context(stream):
             return self._forward_train(x, ws)

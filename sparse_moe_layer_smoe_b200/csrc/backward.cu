@@ -175,9 +175,10 @@ __device__ __forceinline__ void permute_backward_row(const uint4* __restrict__ r
 
 // One CTA per token. The router's term is left out when dlogits is null. With it a token reads 16 KB of the
 // router's weights for each of its experts (at H = 4096), more than the rows themselves, but from L2: 8192
-// tokens take 128 us, 5.2 TB/s of HBM beside as much again and half from L2 (141 us where every pass writes
-// another output, so that no written line is still in L2). Four CTAs an SM matter (three: 139 us, two: 163). Keeping the weights of a 128-feature slice of all experts in shared memory, so that
-// only the rows cross L2, was slower: 228 us, as rows are then read in 256-byte pieces.
+// tokens take 137 to 142 us, 4.9 TB/s of HBM beside as much again and half from L2 (128 us where every pass writes
+// the same output, which then stays in L2; the other figures here are of that kind). Four CTAs an SM matter
+// (three: 139 us, two: 163). Keeping the weights of a 128-feature slice of all experts in shared memory, so
+// that only the rows cross L2, was slower: 228 us, as rows are then read in 256-byte pieces.
 __global__ void __launch_bounds__(256, 4) permute_backward_kernel(const uint16_t* __restrict__ dx_rows,
                                                                const int32_t* __restrict__ perm_row,
                                                                const int32_t* __restrict__ topk_idx,
